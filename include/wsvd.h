@@ -55,7 +55,8 @@ enum { WSVD_DTYPE_FP16 = 0, WSVD_DTYPE_BF16 = 1 };
 enum {
   WSVD_DEVERR_LEN_RANGE = 1,     /* decode: seq_lens[b] < 0 or > L_cap; that sequence's output is 0 */
   WSVD_DEVERR_CACHE_FULL = 2,    /* append: seq_lens[b] >= L_cap (or < 0); row not written, length kept */
-  WSVD_DEVERR_PIPE_TIMEOUT = 4   /* a pipeline wait exceeded its time limit; outputs are not valid */
+  WSVD_DEVERR_PIPE_TIMEOUT = 4,  /* a pipeline wait exceeded its time limit; outputs are not valid */
+  WSVD_DEVERR_PAGE_RANGE = 8     /* paged caches: a page id that a call needs is < 0 or >= num_pages */
 };
 
 /* Human-readable name of a wsvd_status. Never NULL. */
@@ -442,6 +443,89 @@ int shared_latent_svd_decode(int B, int H, int Hd, int R, int L_cap, const int32
                              const void* q, int q_dtype, const void* lat_k, const void* lat_v,
                              const void* B_k, const void* B_v, float softmax_scale, float* out,
                              void* workspace, size_t workspace_bytes, int32_t* err, void* stream);
+
+/* ---------------------------------------------------------------- paged dense cache
+ * The dense 16-bit cache of dense_decode_attention for a server whose sequences
+ * come, grow and leave: keys and values lie in pages of a pool that all
+ * sequences share.  The method's
+ * summaries have no counterpart.
+ *   k_pages, v_pages [num_pages][Hkv][page_size][Hd]  fp16 or bf16 (dtype), at
+ *             most 2^63 bytes; page_size 16, 32, 64, 128 or 256.
+ *   block_table [B][max_pages] int32: rows i * page_size .. (i + 1) * page_size - 1
+ *             of sequence b lie in page block_table[b][i].  Entries that no row
+ *             of a sequence reaches are never read.  Sequences may share pages
+ *             that are only read (a common prefix); a page that receives new
+ *             rows must belong to one sequence.
+ *   A page id < 0 or >= num_pages never faults: WSVD_DEVERR_PAGE_RANGE.
+ *   Hd in {32, 64, 128, 256}; B <= 65535; max_pages * page_size < 2^31.
+ *
+ * paged_kv_append stores T new tokens per sequence and applies the rotary
+ * position rotation on the way: token t of sequence b becomes row
+ * l = seq_lens[b] + t, which is also its position.  The first rot_dim values of
+ * each head of k (and of q) are rotated in pairs,
+ *   a' = a cos - b sin,  b' = b cos + a sin,
+ * cos = cos_sin[l][i], sin = cos_sin[l][rot_dim / 2 + i] for pair
+ * i < rot_dim / 2, which is (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * interleaved != 0; fp32, each result rounded once.  The other values and v
+ * are copied.
+ *   k, v      [B][T][Hkv][Hd], q [B][T][Hq][Hd] of the pages' type; the heads of
+ *             a token are dense, tokens k_stride / v_stride / q_stride values
+ *             apart (multiples of 8; b and t count as one axis), so slices of
+ *             a fused projection's output are taken as they are.
+ *   q_out     [B][T][Hq][Hd], written: the rotated q.  Hq = 0: no q (q, q_out
+ *             NULL).  q_out may be q itself when q is dense.
+ *   rot_dim   0 (no rotation, cos_sin NULL) or a multiple of 16 up to Hd.
+ *   cos_sin   [max_pos][rot_dim] float32; positions >= max_pos have no angle.
+ *   new_lens  [B] int32 or NULL: only the first new_lens[b] <= T tokens of
+ *             sequence b exist (a padded batch); the q_out rows of the others
+ *             are zero and nothing of them is stored.  NULL: all T.
+ *   seq_lens  [B] int32, the rows already cached; seq_lens_out [B] receives
+ *             the new lengths and may be seq_lens itself.
+ *   A sequence whose new rows do not fit (seq_lens[b] < 0, or past
+ *   max_pages * page_size or max_pos) raises WSVD_DEVERR_CACHE_FULL; new_lens[b]
+ *   < 0 or > T raises WSVD_DEVERR_LEN_RANGE; a bad page WSVD_DEVERR_PAGE_RANGE.
+ *   Such a sequence is refused whole: nothing of it is stored, its q_out rows
+ *   are zero and its length is kept.
+ *   workspace at least paged_kv_append_workspace_size(B) bytes, ZERO before the
+ *             first call; every call leaves it zero.  Calls sharing it must not
+ *             overlap.
+ * What is written must not share memory with what is read or with other
+ * outputs, the two in-place cases apart (else WSVD_ERR_INVALID_ARG).
+ * T = 0 only copies the lengths.  One launch.                               */
+size_t paged_kv_append_workspace_size(int B);
+int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int interleaved, int page_size, int num_pages,
+                    int max_pages, int max_pos, const void* k, long long k_stride, const void* v, long long v_stride,
+                    const void* q, long long q_stride, int dtype, const float* cos_sin, const int32_t* new_lens,
+                    const int32_t* block_table, const int32_t* seq_lens, int32_t* seq_lens_out, void* k_pages,
+                    void* v_pages, void* q_out, void* workspace, size_t workspace_bytes, int32_t* err, void* stream);
+/* Attention of the newest tokens over the pages, as dense_decode_attention over
+ * rows and with the queries of wsvd_decode_multi: Hq query heads share Hkv heads
+ * (head g reads head g / (Hq / Hkv)), and query token t of sequence b sees rows
+ * [0, seq_lens[b] - Tq + 1 + t).
+ *   out[b,t,g] = softmax(K . q[b,t,g] * softmax_scale) . V over those rows;
+ *   a query that sees no row gets 0.
+ * fp32 accumulation; the weights enter the product with V with 22 (fp16) or 24
+ * (bf16) significant bits.  Rows >= seq_lens[b] are never read, and rows that a
+ * query does not see never reach it, whatever they hold (infinities and NaN
+ * included).  An infinite value in a row that is seen gives NaN.
+ *   q         [B][Tq][Hq][Hd] of the pages' type (dtype).
+ *   out       [B][Tq][Hq][Hd] float32, written.
+ *   softmax_scale 0 selects 1/sqrt(Hd).
+ *   Hq a multiple of Hkv; Hq / Hkv * Tq <= 64.
+ *   workspace at least paged_decode_workspace_size(...) bytes, ZERO before the
+ *             first call (split partials, one counter per sequence, head and
+ *             group of 8 or 16 queries; every call leaves the counters zero).
+ *             Calls sharing it must not overlap on the GPU.
+ *   err       optional; WSVD_DEVERR_LEN_RANGE for seq_lens[b] < 0 or
+ *             > max_pages * page_size (that sequence's output is 0),
+ *             WSVD_DEVERR_PAGE_RANGE for a bad page (that sequence's output is
+ *             not valid).
+ * One launch.                                                               */
+size_t paged_decode_workspace_size(int B, int Tq, int Hq, int Hkv, int Hd);
+int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size, int num_pages, int max_pages,
+                           const int32_t* seq_lens, const int32_t* block_table, const void* q, const void* k_pages,
+                           const void* v_pages, int dtype, float softmax_scale, float* out, void* workspace,
+                           size_t workspace_bytes, int32_t* err, void* stream);
 
 #ifdef __cplusplus
 }

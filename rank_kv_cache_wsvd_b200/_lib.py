@@ -20,8 +20,10 @@ WSVD_DTYPE_BF16 = 1
 DEVERR_LEN_RANGE = 1
 DEVERR_CACHE_FULL = 2
 DEVERR_PIPE_TIMEOUT = 4
+DEVERR_PAGE_RANGE = 8
 
 _c_int, _c_size, _c_float, _p = ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes); every symbol the public header declares.
 SIGNATURES = {
@@ -62,6 +64,10 @@ SIGNATURES = {
                                   + [_c_float, _p, _p, _c_size, _p, _c_size, _p, _p]),
     "wsvd_fold_latent_rotation": (_c_int, [_c_int] * 4 + [_p] * 11),
     "dense_decode_attention": (_c_int, [_c_int] * 4 + [_p, _p, _c_int, _p, _p, _c_float, _p, _p, _c_size, _p, _p]),
+    "paged_kv_append_workspace_size": (_c_size, [_c_int]),
+    "paged_kv_append": (_c_int, [_c_int] * 11 + [_p, _c_ll] * 3 + [_c_int] + [_p] * 9 + [_c_size, _p, _p]),
+    "paged_decode_workspace_size": (_c_size, [_c_int] * 5),
+    "paged_decode_attention": (_c_int, [_c_int] * 8 + [_p] * 5 + [_c_int, _c_float, _p, _p, _c_size, _p, _p]),
     "shared_latent_svd_decode": (_c_int, [_c_int] * 5 + [_p, _p, _c_int] + [_p] * 4 + [_c_float, _p, _p, _c_size,
                                                                                          _p, _p]),
 }
@@ -299,6 +305,158 @@ def shared_latent_svd_decode(q, lat_k, lat_v, B_k, B_v, seq_lens, softmax_scale:
                                       _ptr(lat_v), _ptr(B_k), _ptr(B_v), float(softmax_scale), _ptr(out),
                                       _ptr(workspace_buf), workspace_buf.numel(), _ptr(err), _stream(stream))
     _check(st, "shared_latent_svd_decode")
+    return out
+
+
+# ----------------------------------------------------------------------------- paged dense cache
+class _Device:
+    """The device that every tensor of a call lies on, made current for the call
+    (the library launches on the current device) when another one is."""
+
+    def __init__(self, t, stream=None):
+        if not t.is_cuda:
+            raise WsvdError("all tensors must be CUDA tensors")
+        self.index = t.get_device()
+        if stream is not None and stream.device_index != self.index:
+            raise WsvdError(f"stream: expected one of cuda:{self.index}, got one of cuda:{stream.device_index}")
+        self._stream = stream
+        self._back = torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.index != self._back:
+            torch.cuda.set_device(self.index)
+        return self
+
+    def __exit__(self, *exc):
+        if self.index != self._back:
+            torch.cuda.set_device(self._back)
+
+    def new(self, make, shape, dtype):
+        """A tensor made on the call's stream, so that its memory and its fill
+        are ordered with the launch."""
+        if self._stream is None:
+            return make(shape, dtype=dtype, device="cuda")
+        with torch.cuda.stream(self._stream):
+            return make(shape, dtype=dtype, device="cuda")
+
+    def dense(self, t, dtype, shape, name):
+        """Address of a dense tensor of this device with the dtype and shape given."""
+        if t.dtype != dtype or t.shape != shape:
+            raise WsvdError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != self.index:
+            raise WsvdError(f"{name}: expected a tensor on cuda:{self.index}, got {t.device}")
+        if not t.is_contiguous():
+            raise WsvdError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def tokens(self, t, dtype, shape, name):
+        """Address and token stride of [B][T][heads][Hd] whose heads are dense and
+        whose batch and token axes step as one (a slice of a fused projection)."""
+        if t.dtype != dtype or t.shape != shape:
+            raise WsvdError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != self.index:
+            raise WsvdError(f"{name}: expected a tensor on cuda:{self.index}, got {t.device}")
+        B, T, heads, Hd = shape
+        sb, st, sh, sd = t.stride()
+        if T == 1:
+            st = sb if B > 1 else heads * Hd
+        if t.numel() and (sd != 1 or (heads > 1 and sh != Hd) or (B > 1 and sb != T * st)):
+            raise WsvdError(f"{name}: the heads of a token must be dense and tokens evenly spaced, "
+                            f"got strides {tuple(t.stride())}")
+        return t.data_ptr(), st if t.numel() else heads * Hd
+
+    def optional(self, t, dtype, shape, name):
+        return None if t is None else self.dense(t, dtype, shape, name)
+
+    def scratch(self, t, nbytes):
+        """Address and bytes of the caller's workspace, or of a new zeroed one."""
+        if t is None:
+            t = self.new(torch.zeros, (max(16, nbytes),), torch.uint8)
+        return self.dense(t, torch.uint8, t.shape, "workspace_buf"), t.numel(), t
+
+    def error_word(self, err):
+        return None if err is None else self.dense(err, torch.int32, err.shape, "err")
+
+    def stream(self):
+        return (self._stream or torch.cuda.current_stream()).cuda_stream
+
+
+def paged_kv_append_workspace_size(B) -> int:
+    return load().paged_kv_append_workspace_size(B)
+
+
+def paged_decode_workspace_size(B, Tq, Hq, Hkv, Hd) -> int:
+    return load().paged_decode_workspace_size(B, Tq, Hq, Hkv, Hd)
+
+
+def paged_kv_append(k, v, k_pages, v_pages, block_table, seq_lens, q=None, q_out=None, cos_sin=None,
+                    interleaved: bool = False, new_lens=None, seq_lens_out=None, workspace_buf=None, err=None,
+                    stream=None):
+    """Store T new tokens per sequence (k, v [B][T][Hkv][Hd]) in the pages that
+    block_table names, at rows seq_lens[b] .. , with the rotary rotation of
+    cos_sin [max_pos][rot_dim] (cosines, then sines) applied to k and to q
+    [B][T][Hq][Hd].  Lengths advance in place unless seq_lens_out is given.
+    Returns q_out (None without q)."""
+    lib = load()
+    B, T, Hkv, Hd = k.shape
+    num_pages, _, page_size, _ = k_pages.shape
+    max_pages = block_table.shape[1]
+    dtype, code = k.dtype, _dtype_code(k)
+    with _Device(k, stream) as dev:
+        pk, sk = dev.tokens(k, dtype, (B, T, Hkv, Hd), "k")
+        pv, sv = dev.tokens(v, dtype, (B, T, Hkv, Hd), "v")
+        Hq, pq, sq, po = 0, None, 0, None
+        if q is not None:
+            Hq = q.shape[2]
+            pq, sq = dev.tokens(q, dtype, (B, T, Hq, Hd), "q")
+            if q_out is None:
+                q_out = dev.new(torch.empty, (B, T, Hq, Hd), dtype)
+            po = dev.dense(q_out, dtype, (B, T, Hq, Hd), "q_out")
+        elif q_out is not None:
+            raise WsvdError("q_out without q")
+        max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+        if seq_lens_out is None:
+            seq_lens_out = seq_lens
+        ws, ws_bytes, keep = dev.scratch(workspace_buf, lib.paged_kv_append_workspace_size(B))
+        st = lib.paged_kv_append(
+            B, T, Hq, Hkv, Hd, rot, int(interleaved), page_size, num_pages, max_pages, max_pos, pk, sk, pv, sv, pq, sq,
+            code, dev.optional(cos_sin, torch.float32, (max_pos, rot), "cos_sin"),
+            dev.optional(new_lens, torch.int32, (B,), "new_lens"),
+            dev.dense(block_table, torch.int32, (B, max_pages), "block_table"),
+            dev.dense(seq_lens, torch.int32, (B,), "seq_lens"),
+            dev.dense(seq_lens_out, torch.int32, (B,), "seq_lens_out"),
+            dev.dense(k_pages, dtype, (num_pages, Hkv, page_size, Hd), "k_pages"),
+            dev.dense(v_pages, dtype, (num_pages, Hkv, page_size, Hd), "v_pages"), po, ws, ws_bytes,
+            dev.error_word(err), dev.stream())
+    _check(st, "paged_kv_append")
+    return q_out
+
+
+def paged_decode_attention(q, k_pages, v_pages, block_table, seq_lens, softmax_scale: float = 0.0, out=None,
+                           workspace_buf=None, err=None, stream=None):
+    """Attention of the newest Tq tokens, q [B][Tq][Hq][Hd] (or [B][Hq][Hd]: one),
+    over k_pages, v_pages [num_pages][Hkv][page_size][Hd]; query token t sees
+    rows [0, seq_lens[b] - Tq + 1 + t).  Returns out, fp32, in q's shape."""
+    lib = load()
+    if q.dim() == 4:
+        B, Tq, Hq, Hd = q.shape
+    else:
+        B, Hq, Hd = q.shape
+        Tq = 1
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    max_pages = block_table.shape[1]
+    dtype, code = q.dtype, _dtype_code(q)
+    with _Device(q, stream) as dev:
+        if out is None:
+            out = dev.new(torch.empty, q.shape, torch.float32)
+        ws, ws_bytes, keep = dev.scratch(workspace_buf, lib.paged_decode_workspace_size(B, Tq, Hq, Hkv, Hd))
+        st = lib.paged_decode_attention(
+            B, Tq, Hq, Hkv, Hd, page_size, num_pages, max_pages, dev.dense(seq_lens, torch.int32, (B,), "seq_lens"),
+            dev.dense(block_table, torch.int32, (B, max_pages), "block_table"), dev.dense(q, dtype, q.shape, "q"),
+            dev.dense(k_pages, dtype, (num_pages, Hkv, page_size, Hd), "k_pages"),
+            dev.dense(v_pages, dtype, (num_pages, Hkv, page_size, Hd), "v_pages"), code, softmax_scale,
+            dev.dense(out, torch.float32, q.shape, "out"), ws, ws_bytes, dev.error_word(err), dev.stream())
+    _check(st, "paged_decode_attention")
     return out
 
 

@@ -1,0 +1,891 @@
+// Dense 16-bit key-value cache in pages, for sm_100a: appending new keys and
+// values with the rotary position rotation, and attention of the newest
+// token(s) over the pages.
+//
+// A cache is a pool of pages [num_pages][Hkv][page_size][Hd] shared by all
+// sequences; block_table[b][i] names the page that holds rows
+// i * page_size .. of sequence b, so row l of head h lies at
+//   pool + ((block_table[b][l / page_size] * Hkv + h) * page_size + l % page_size) * Hd.
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <tuple>
+
+#include "common.cuh"
+
+using namespace wsvd;
+
+namespace {
+
+// ------------------------------------------------------------------ append
+struct KvAppendArgs {
+  int T, Hq, Hkv, Hd, rot, inter, page_shift, num_pages, max_pages, cap;
+  int tokens;  // tokens per CTA
+  const uint16_t *k, *v, *q;
+  long long k_stride, v_stride, q_stride;
+  const float* cos_sin;
+  const int32_t* new_lens;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t* seq_lens_out;
+  uint16_t *k_pages, *v_pages, *q_out;
+  int32_t* counters;
+  int32_t* err;
+};
+
+constexpr int kAppendCta = 256;
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return h2_pair(w);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// The rotation of 8 pairs (a_i, b_i): a' = a cos - b sin, b' = b cos + a sin,
+// in fp32, rounded once to the 16-bit type of the cache.  x, y: the two
+// 16-byte chunks of a unit.  Split pairs: a_i in x, b_i in y; interleaved: the
+// pairs lie side by side, four in x, four in y.
+template <bool BF16>
+__device__ __forceinline__ void rotate_unit(uint4& x, uint4& y, const float4* cs, const float4* sn, bool inter) {
+  uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+  uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+  const float* c = reinterpret_cast<const float*>(cs);
+  const float* s = reinterpret_cast<const float*>(sn);
+  if (inter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = unpack2<BF16>(xw[i]), w = unpack2<BF16>(yw[i]);
+      xw[i] = pack2<BF16>(u.x * c[i] - u.y * s[i], u.y * c[i] + u.x * s[i]);
+      yw[i] = pack2<BF16>(w.x * c[4 + i] - w.y * s[4 + i], w.y * c[4 + i] + w.x * s[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = unpack2<BF16>(xw[i]), w = unpack2<BF16>(yw[i]);
+      const float c0 = c[2 * i], c1 = c[2 * i + 1], s0 = s[2 * i], s1 = s[2 * i + 1];
+      xw[i] = pack2<BF16>(u.x * c0 - w.x * s0, u.y * c1 - w.y * s1);
+      yw[i] = pack2<BF16>(w.x * c0 + u.x * s0, w.y * c1 + u.y * s1);
+    }
+  }
+}
+
+// grid (token tiles, B).  A unit is 32 bytes of one head's row: the two 16-byte
+// chunks whose values are rotated together (split pairs: chunks i and
+// i + rot/16), or two neighbouring chunks.
+template <bool BF16>
+__global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArgs a) {
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int pos = a.seq_lens[b];
+  const int n = a.new_lens ? a.new_lens[b] : a.T;
+  // The whole block of a sequence is refused together, so every CTA of the
+  // sequence comes to the same answer before it writes.
+  const bool len_ok = n >= 0 && n <= a.T;
+  bool ok = len_ok && pos >= 0 && (long long)pos + n <= a.cap;
+  const int32_t* table = a.block_table + (size_t)b * a.max_pages;
+  bool bad_page = false;
+  if (ok && n > 0) {
+    const int p1 = (pos + n - 1) >> a.page_shift;
+    for (int p = (pos >> a.page_shift) + tid; p <= p1; p += kAppendCta) {
+      const int pg = table[p];
+      bad_page |= pg < 0 || pg >= a.num_pages;
+    }
+  }
+  bad_page = __syncthreads_or(bad_page);
+  if (tid == 0 && blockIdx.x == 0) {
+    if (!len_ok) set_err(a.err, WSVD_DEVERR_LEN_RANGE);
+    else if (!ok) set_err(a.err, WSVD_DEVERR_CACHE_FULL);
+    else if (bad_page) set_err(a.err, WSVD_DEVERR_PAGE_RANGE);
+  }
+  ok = ok && !bad_page;
+  const int there = ok ? n : 0;
+
+  const int units = a.Hd / 16, rows = a.Hq + 2 * a.Hkv, ru = a.rot / 16;
+  const int t0 = blockIdx.x * a.tokens, t1 = min(a.T, t0 + a.tokens);
+  const int mask = (1 << a.page_shift) - 1;
+  const int unit = tid % units, slot = tid / units, slots = kAppendCta / units;
+  const bool turned = unit < ru;
+  const int c0 = turned && !a.inter ? unit : 2 * unit, c1 = turned && !a.inter ? unit + ru : 2 * unit + 1;
+  for (int i = slot; i < (t1 - t0) * rows; i += slots) {
+    const int t = t0 + i / rows, row = i % rows;
+    const size_t tok = (size_t)b * a.T + t;
+    if (t >= there) {  // padding: nothing is cached, q_out is zero
+      if (row < a.Hq) {
+        uint4* dst = reinterpret_cast<uint4*>(a.q_out + (tok * a.Hq + row) * a.Hd);
+        dst[c0] = dst[c1] = make_uint4(0, 0, 0, 0);
+      }
+      continue;
+    }
+    const int l = pos + t;
+    const uint16_t* src;
+    uint16_t* out;
+    if (row < a.Hq) {
+      src = a.q + tok * a.q_stride + (size_t)row * a.Hd;
+      out = a.q_out + (tok * a.Hq + row) * a.Hd;
+    } else {
+      const int h = (row - a.Hq) % a.Hkv;
+      const bool is_v = row >= a.Hq + a.Hkv;
+      src = (is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) + (size_t)h * a.Hd;
+      const size_t at = ((((size_t)table[l >> a.page_shift] * a.Hkv + h) << a.page_shift) + (l & mask)) * a.Hd;
+      out = (is_v ? a.v_pages : a.k_pages) + at;
+    }
+    uint4 x = reinterpret_cast<const uint4*>(src)[c0], y = reinterpret_cast<const uint4*>(src)[c1];
+    if (turned && row < a.Hq + a.Hkv) {
+      const float4* cs = reinterpret_cast<const float4*>(a.cos_sin + (size_t)l * a.rot) + 2 * unit;
+      const float4* sn = cs + a.rot / 8;
+      const float4 c[2] = {cs[0], cs[1]}, s[2] = {sn[0], sn[1]};
+      rotate_unit<BF16>(x, y, c, s, a.inter);
+    }
+    reinterpret_cast<uint4*>(out)[c0] = x;
+    reinterpret_cast<uint4*>(out)[c1] = y;
+  }
+
+  // The new length.  Written in place it must not be seen by a CTA of this
+  // sequence that has not read the old one: the last CTA to arrive writes it.
+  if (tid == 0) {
+    const int len = there ? pos + there : pos;
+    if (a.seq_lens_out != a.seq_lens) {
+      if (blockIdx.x == 0) a.seq_lens_out[b] = len;
+    } else if (gridDim.x == 1) {
+      a.seq_lens_out[b] = len;
+    } else if (atom_add_acq_rel_gpu(a.counters + b, 1) == (int)gridDim.x - 1) {
+      st_relaxed_gpu(a.seq_lens_out + b, len);
+      st_relaxed_gpu(a.counters + b, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ decode
+// For each sequence b, KV head h and chunk of its G * Tq queries the rows are
+// cut into strips of TS rows.  All strips of all (b, h, chunk) units, in that
+// order, are dealt evenly to a grid of CTAs; a CTA's share of one unit is a
+// segment, whose strips its warps take in turn.  Each warp is a pipeline of its
+// own: it copies its strips with cp.async into its ring in shared memory
+// (16-byte chunks, swizzled so that ldmatrix reads no bank twice) and needs no
+// barrier until the segment ends.
+//
+// Per strip, with m16n8k16 products (rows x queries, so up to 8 queries cost
+// one column block, and GQA reads the rows once for all of them):
+//   S = K q^T         K as the row operand, q^T held in registers
+//   p = 2^(S * scale * log2 e - m), m the running maximum of the warp's rows
+//   O^T += V^T p^T    V^T by transposed ldmatrix, p^T by movmatrix
+// p is not rounded to the 16-bit type: it is cut into parts whose sum carries
+// 22 (two fp16 parts) or 24 bits (three bf16 parts), each its own product.
+// The products cost less than the rows' bytes for up to 16 queries.
+template <bool BF16, int HD, int NB>
+struct DecCfg {
+  static constexpr int kWarps = 4;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kTS = HD >= 128 ? 16 : (HD == 64 ? 32 : 64);  // rows per strip
+  static constexpr int kMT = kTS / 16;
+  static constexpr int kStages = 3;
+  static constexpr int kHalf = kTS * HD * 2;      // bytes of a strip's K (or V)
+  static constexpr int kStage = 2 * kHalf;
+
+  static constexpr int kChunks = HD / 8;          // 16-byte chunks of a row
+  static constexpr int kParts = BF16 ? 3 : 2;
+  static constexpr int kQ = 8 * NB;               // queries of a chunk
+  static constexpr int kPitch = HD + 4;           // floats per query in the merge scratch
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+  static_assert(kPitch * 8 * 4 <= kStage, "a warp's merge scratch is one stage");
+};
+
+struct KvDecodeArgs {
+  int B, Tq, Hq, Hkv, G, nq, chunks, page_shift, num_pages, max_pages, cap, ctas;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  const uint16_t *q, *k, *v;
+  float* out;
+  float* partials;  // [2 * ctas][min(nq, kQ)][HD + 2]
+  int32_t* counters;
+  int32_t* err;
+  float qscale;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movm_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk c of row r in a strip: eight rows at one chunk
+// index lie in eight different 16-byte columns of the banks.
+template <int HD>
+__device__ __forceinline__ uint32_t strip_off(int r, int c) {
+  if (HD == 32) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)(r * HD * 2 + ((c ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ int valid_len(const KvDecodeArgs& a, int b) {
+  const int n = a.seq_lens[b];
+  return n < 0 || n > a.cap ? 0 : n;
+}
+
+// A segment: strips [s, e) of unit u (KV head * chunks + chunk) of sequence b.
+template <int TS>
+struct Segment {
+  int b, u, n, s, e;
+  long long left;  // strips of the CTA's share from s on
+  __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
+  __device__ __forceinline__ bool next(const KvDecodeArgs& a) {
+    left -= e - s;
+    if (left <= 0) return false;
+    if (++u == a.Hkv * a.chunks) {
+      u = 0;
+      do n = valid_len(a, ++b);
+      while (n == 0);
+    }
+    s = 0;
+    e = (int)min((long long)strips(), left);
+    return true;
+  }
+};
+
+template <bool BF16, int HD, int NB>
+__global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
+  using C = DecCfg<BF16, HD, NB>;
+  constexpr int TS = C::kTS, MT = C::kMT, S = C::kStages, NW = C::kWarps, KS = HD / 16, NP = C::kParts;
+  // 2^bias keeps the low fp16 part of small weights out of the denormals.
+  constexpr float kBias = BF16 ? 0.f : 12.f;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ long long scan[NW];
+  __shared__ int start_b;
+  __shared__ long long start_rem;
+  __shared__ float sm_m[NW][C::kQ], sm_l[NW][C::kQ];
+  __shared__ int sm_valid[NW][S];
+  __shared__ int sm_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
+  const int c = blockIdx.x, units = a.Hkv * a.chunks;
+
+  // The strips of all sequences, and where this CTA's share starts.
+  const int per = (a.B + C::kThreads - 1) / C::kThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int raw = a.seq_lens[b];
+    if ((raw < 0 || raw > a.cap) && c == 0) set_err(a.err, WSVD_DEVERR_LEN_RANGE);
+    sum += (valid_len(a, b) + TS - 1) / TS;
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long total = 0, before = incl - sum;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const long long G = total * units;
+  // Sequences without rows: zeros, spread over the CTAs.
+  for (int b = c; b < a.B; b += gridDim.x)
+    if (valid_len(a, b) == 0)
+      for (int i = tid; i < a.Tq * a.Hq * HD; i += C::kThreads) a.out[(size_t)b * a.Tq * a.Hq * HD + i] = 0.f;
+  // At least one strip per warp, so that a small problem is not cut too finely.
+  const long long most = (G + NW - 1) / NW;
+  const int CW = (int)(most < a.ctas ? most : a.ctas);
+  if (c >= CW) return;
+  const long long g_begin = G * c / CW, g_end = G * (c + 1) / CW;
+  if (g_begin >= before * units && g_begin < (before + sum) * units) {
+    long long rem = g_begin - before * units;
+    int b = b0;
+    for (;; ++b) {
+      const long long ns = (long long)((valid_len(a, b) + TS - 1) / TS) * units;
+      if (rem < ns) break;
+      rem -= ns;
+    }
+    start_b = b;
+    start_rem = rem;
+  }
+  __syncthreads();
+
+  Segment<TS> seg;
+  seg.b = start_b;
+  seg.n = valid_len(a, seg.b);
+  seg.u = (int)(start_rem / seg.strips());
+  seg.s = (int)(start_rem % seg.strips());
+  seg.left = g_end - g_begin;
+  seg.e = (int)min((long long)seg.strips(), seg.s + seg.left);
+
+  // ---- the warp's copies: cursor `ld`, page ids one strip ahead
+  const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
+  Segment<TS> ld = seg;
+  int ls = ld.s + warp;
+  bool more = true;
+  int pg[MT];
+  const int page_mask = (1 << a.page_shift) - 1;
+  auto settle = [&]() {  // the next strip of this warp, and its pages
+    while (more && ls >= ld.e) {
+      more = ld.next(a);
+      ls = ld.s + warp;
+    }
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int l = ls * TS + i * 16;
+        pg[i] = l < ld.n ? __ldg(a.block_table + (size_t)ld.b * a.max_pages + (l >> a.page_shift)) : 0;
+      }
+    }
+  };
+  auto issue = [&](int stage) {
+    if (more) {
+      const uint32_t dst = my_ring + (uint32_t)stage * C::kStage;
+      const int h = ld.u / a.chunks;
+      int valid = 0;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int l0 = ls * TS + i * 16;
+        const bool in = pg[i] >= 0 && pg[i] < a.num_pages;
+        if (!in && lane == 0 && l0 < ld.n) set_err(a.err, WSVD_DEVERR_PAGE_RANGE);
+        valid |= (in ? 1 : 0) << i;
+        const size_t row0 = (((size_t)(in ? pg[i] : 0) * a.Hkv + h) << a.page_shift) + (l0 & page_mask);
+        const int rows = in ? ld.n - l0 : 0;  // rows at and past the length are zero-filled, not read
+        constexpr int kPer = 16 * C::kChunks / 32;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int idx = j * 32 + lane, r = idx / C::kChunks, ch = idx % C::kChunks;
+          const uint32_t off = strip_off<HD>(i * 16 + r, ch);
+          const bool there = r < rows;
+          const size_t src = (row0 + (there ? r : 0)) * HD + ch * 8;
+          cp_async16(dst + off, a.k + src, there ? 16u : 0u);
+          cp_async16(dst + C::kHalf + off, a.v + src, there ? 16u : 0u);
+        }
+      }
+      if (lane == 0) sm_valid[warp][stage] = valid;
+      ls += NW;
+      settle();
+    }
+    cp_commit();
+  };
+  settle();
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  int stage = 0;  // of the next strip to read
+
+  // ---- segment by segment
+  bool first_segment = true;
+  for (bool go = true; go;) {
+    const int h = seg.u / a.chunks, j0 = (seg.u % a.chunks) * C::kQ;
+    const int nq = min(C::kQ, a.nq - j0);
+    uint32_t qf[NB][KS][2];
+    int lim[NB][2];  // rows that query 2 * c4 + {0, 1} of a block sees
+    const int lim_min = seg.n - a.Tq + 1;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int j = nb * 8 + g;
+      const int jq = j0 + (j < nq ? j : 0);
+      const uint16_t* qr = a.q + (((size_t)seg.b * a.Tq + jq / a.G) * a.Hq + h * a.G + jq % a.G) * HD + 2 * c4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[nb][k][0] = j < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k)) : 0u;
+        qf[nb][k][1] = j < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8)) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lim[nb][i] = lim_min + min(j0 + nb * 8 + 2 * c4 + i, a.nq - 1) / a.G;
+    }
+    float m[NB][2], l[NB][2], o[KS][NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb][0] = m[nb][1] = kNegInf;
+      l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < KS; ++d) o[d][nb][0] = o[d][nb][1] = o[d][nb][2] = o[d][nb][3] = 0.f;
+    }
+
+    int last_stage = stage == 0 ? S - 1 : stage - 1;  // a stage with nothing in it or on its way
+    for (int s = seg.s + warp; s < seg.e; s += NW) {
+      cp_wait<S - 2>();
+      __syncwarp();
+      issue(stage == 0 ? S - 1 : stage - 1);
+      const uint32_t kb = my_ring + (uint32_t)stage * C::kStage, vb = kb + C::kHalf;
+      float sc[MT][NB][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[t][nb][0] = sc[t][nb][1] = sc[t][nb][2] = sc[t][nb][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t kf[4];
+          ldsm4(kf, kb + strip_off<HD>(t * 16 + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(sc[t][nb], kf, qf[nb][k][0], qf[nb][k][1]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][nb][i] *= a.qscale;
+      const int l0 = s * TS, valid = sm_valid[warp][stage];
+      const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
+      if (masked) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = l0 + t * 16 + g + (i >> 1) * 8;
+              if (row >= lim[nb][i & 1] || !((valid >> t) & 1)) sc[t][nb][i] = kNegInf;
+            }
+      }
+      // Running maximum and sum; columns (queries) of sc and o are the same.
+      uint32_t pf[MT][NB][NP][2];
+      bool moved = false;
+      float alpha[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx = kNegInf;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) mx = fmaxf(mx, fmaxf(sc[t][nb][i], sc[t][nb][i + 2]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          const float mn = fmaxf(m[nb][i], mx);
+          const float ref = mn == kNegInf ? 0.f : mn;
+          alpha[nb][i] = ex2(m[nb][i] - ref);
+          moved |= mn != m[nb][i];
+          m[nb][i] = mn;
+          float add = 0.f;
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; r += 2) {
+              const float p = ex2(sc[t][nb][i + r] - ref + kBias);
+              sc[t][nb][i + r] = p;
+              add += p;
+            }
+          l[nb][i] = l[nb][i] * alpha[nb][i] + add;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int d = 0; d < KS; ++d)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][nb][i] *= alpha[nb][i & 1];
+      }
+      // A later token's value may be infinite or NaN; it must not reach the
+      // queries that do not see it (0 * NaN), so such a strip is summed row by
+      // row.  Rows past the length are zero already.
+      bool wild = false;
+      if (masked && a.Tq > 1) {
+        for (int i = lane; i < TS * C::kChunks; i += 32) {
+          const uint4 w = lds128(vb + (uint32_t)i * 16);
+          const uint32_t e = BF16 ? 0x7f80u : 0x7c00u, e2 = e << 16;
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) wild |= (ws[k] & e) == e || (ws[k] & e2) == e2;
+        }
+        wild = __any_sync(0xffffffffu, wild);
+      }
+      if (wild) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll 1
+          for (int r = 0; r < 16; ++r) {
+            const int row = l0 + t * 16 + r;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const int from = (r & 7) * 4 + c4;
+              const float p00 = __shfl_sync(0xffffffffu, sc[t][nb][0], from);
+              const float p01 = __shfl_sync(0xffffffffu, sc[t][nb][1], from);
+              const float p10 = __shfl_sync(0xffffffffu, sc[t][nb][2], from);
+              const float p11 = __shfl_sync(0xffffffffu, sc[t][nb][3], from);
+              const float p[2] = {r < 8 ? p00 : p10, r < 8 ? p01 : p11};
+#pragma unroll
+              for (int d = 0; d < KS; ++d)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint16_t w;
+                  asm volatile("ld.shared.u16 %0, [%1];"
+                               : "=h"(w)
+                               : "r"(vb + strip_off<HD>(t * 16 + r, 2 * d + half) + 2u * g)
+                               : "memory");
+                  const float v = BF16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (row < lim[nb][i]) o[d][nb][2 * half + i] = fmaf(p[i], v, o[d][nb][2 * half + i]);
+                }
+            }
+          }
+      } else {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float r0 = sc[t][nb][0], r1 = sc[t][nb][1], r2 = sc[t][nb][2], r3 = sc[t][nb][3];
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+              const uint32_t x = pack2<BF16>(r0, r1), y = pack2<BF16>(r2, r3);
+              pf[t][nb][k][0] = movm_t(x);
+              pf[t][nb][k][1] = movm_t(y);
+              const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
+              r0 -= fx.x; r1 -= fx.y; r2 -= fy.x; r3 -= fy.y;
+            }
+          }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int d = 0; d < KS; ++d) {
+            uint32_t vf[4];
+            ldsm4_t(vf, vb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int k = 0; k < NP; ++k) mma16816<BF16>(o[d][nb], vf, pf[t][nb][k][0], pf[t][nb][k][1]);
+          }
+      }
+      __syncwarp();  // every lane has read this stage before it is filled again
+      last_stage = stage;
+      stage = stage == S - 1 ? 0 : stage + 1;
+    }
+
+    // ---- the warps' results of this segment: m, l and O joined
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = l[nb][i];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        if (g == 0) {
+          sm_m[warp][nb * 8 + 2 * c4 + i] = m[nb][i];
+          sm_l[warp][nb * 8 + 2 * c4 + i] = v;
+        }
+      }
+    __syncthreads();
+    const int ns = seg.strips();
+    const bool whole = seg.s == 0 && seg.e == ns;
+    const int qmax = min(C::kQ, a.nq);  // queries per partial slot
+    float* part = a.partials + (size_t)(2 * c + (first_segment ? 0 : 1)) * qmax * (HD + 2);
+    float* scratch = reinterpret_cast<float*>(ring);
+    const uint32_t my_scratch = (uint32_t)(warp * S + last_stage) * (C::kStage / 4);
+    __shared__ int sm_slot[NW];
+    if (lane == 0) sm_slot[warp] = warp * S + last_stage;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if (nb * 8 >= nq) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = nb * 8 + 2 * c4 + i;
+        float M = kNegInf;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w][j]);
+        const float f = ex2(m[nb][i] - (M == kNegInf ? 0.f : M));
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+          scratch[my_scratch + (2 * c4 + i) * C::kPitch + d * 16 + g] = o[d][nb][i] * f;
+          scratch[my_scratch + (2 * c4 + i) * C::kPitch + d * 16 + 8 + g] = o[d][nb][2 + i] * f;
+        }
+      }
+      __syncthreads();
+      const int here = min(8, nq - nb * 8);
+      for (int idx = tid; idx < here * HD; idx += C::kThreads) {
+        const int jj = idx / HD, d = idx % HD, j = nb * 8 + jj;
+        float M = kNegInf, L = 0.f, sumo = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w][j]);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          L += sm_l[w][j] * ex2(sm_m[w][j] - (M == kNegInf ? 0.f : M));
+          sumo += scratch[(size_t)sm_slot[w] * (C::kStage / 4) + jj * C::kPitch + d];
+        }
+        if (whole) {
+          const int jq = j0 + j, t = jq / a.G;
+          a.out[(((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d] =
+              lim_min + t > 0 ? sumo / L : 0.f;
+        } else {
+          part[j * (HD + 2) + 2 + d] = sumo;
+          if (d == 0) {
+            part[j * (HD + 2)] = M;
+            part[j * (HD + 2) + 1] = L;
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- a unit cut over several CTAs: the last to arrive joins the partials
+    // in the order of the CTAs, so the result does not depend on who that is.
+    if (!whole) {
+      const long long u0 = g_end - seg.left - seg.s, u1 = u0 + ns;  // the unit's strips in the whole order
+      const int cf = (int)(((u0 + 1) * CW - 1) / G), cl = (int)((u1 * CW - 1) / G);
+      const size_t unit = (size_t)seg.b * units + seg.u;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + unit, 1) == cl - cf;
+      __syncthreads();
+      if (sm_last) {
+        __threadfence();
+        // the unit is the first segment of every CTA but perhaps the first one
+        const bool cf_first = G * cf / CW == u0;
+        const size_t slot = (size_t)qmax * (HD + 2);
+        for (int idx = tid; idx < nq * HD; idx += C::kThreads) {
+          const int j = idx / HD, d = idx % HD;
+          float M = kNegInf, L = 0.f, sumo = 0.f;
+          for (int cc = cf; cc <= cl; ++cc) {
+            const float* p = a.partials + (size_t)(2 * cc + (cc > cf || cf_first ? 0 : 1)) * slot + j * (HD + 2);
+            M = fmaxf(M, __ldcg(p));
+          }
+          for (int cc = cf; cc <= cl; ++cc) {
+            const float* p = a.partials + (size_t)(2 * cc + (cc > cf || cf_first ? 0 : 1)) * slot + j * (HD + 2);
+            const float f = ex2(__ldcg(p) - (M == kNegInf ? 0.f : M));
+            L = fmaf(__ldcg(p + 1), f, L);
+            sumo = fmaf(__ldcg(p + 2 + d), f, sumo);
+          }
+          const int jq = j0 + j, t = jq / a.G;
+          a.out[(((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d] =
+              lim_min + t > 0 ? sumo / L : 0.f;
+        }
+        if (tid == 0) st_relaxed_gpu(a.counters + unit, 0);
+      }
+    }
+    go = seg.next(a);
+    first_segment = false;
+  }
+  cp_wait<0>();
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
+inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Whether [p, p + np) and [q, q + nq) share a byte.
+inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return np && nq && a < b + nq && b < a + np;
+}
+
+// Upper bound of the decode's grid; sizes its partials.
+constexpr int kMaxPagedCtas = 592;
+
+// Queries per chunk: two column blocks of 8, one at head size 256 (registers).
+inline int chunk_queries(int nq, int Hd) { return nq > 8 && Hd != 256 ? 16 : 8; }
+
+using DecodeFn = void (*)(const KvDecodeArgs);
+struct DecodeKernel {
+  DecodeFn fn;
+  size_t smem;
+  int threads;
+};
+template <bool BF16, int HD, int NB>
+DecodeKernel decode_kernel_of() {
+  using C = DecCfg<BF16, HD, NB>;
+  return DecodeKernel{&kv_decode_kernel<BF16, HD, NB>, C::kSmem, C::kThreads};
+}
+template <bool BF16>
+DecodeKernel pick_decode(int Hd, int qc) {
+  switch (Hd) {
+    case 32: return qc == 16 ? decode_kernel_of<BF16, 32, 2>() : decode_kernel_of<BF16, 32, 1>();
+    case 64: return qc == 16 ? decode_kernel_of<BF16, 64, 2>() : decode_kernel_of<BF16, 64, 1>();
+    case 128: return qc == 16 ? decode_kernel_of<BF16, 128, 2>() : decode_kernel_of<BF16, 128, 1>();
+    default: return decode_kernel_of<BF16, 256, 1>();
+  }
+}
+
+// SM count and resident CTAs of a kernel on the current device (the shared
+// memory opt-in is made on the way), asked once per device and kernel.
+cudaError_t resident_ctas(const DecodeKernel& k, int* ctas) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(dev, reinterpret_cast<const void*>(k.fn));
+  auto it = known.find(key);
+  if (it == known.end()) {
+    int sms = 0, occ = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(key.second, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, k.threads, k.smem);
+    if (e != cudaSuccess) return e;
+    it = known.emplace(key, std::min(kMaxPagedCtas, sms * std::max(1, occ))).first;
+  }
+  *ctas = it->second;
+  return cudaSuccess;
+}
+
+int page_shift_of(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+struct DecodeWs {
+  size_t partials, counters, total;
+};
+DecodeWs decode_ws(int B, int Tq, int Hq, int Hkv, int Hd) {
+  const int nq = Hq / Hkv * Tq, qc = chunk_queries(nq, Hd), chunks = (nq + qc - 1) / qc;
+  DecodeWs w;
+  w.partials = 0;
+  w.counters = align16((size_t)2 * kMaxPagedCtas * std::min(nq, qc) * (Hd + 2) * sizeof(float));
+  w.total = w.counters + align16((size_t)B * Hkv * chunks * sizeof(int32_t));
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t paged_kv_append_workspace_size(int B) { return B < 0 ? 0 : std::max<size_t>(16, align16((size_t)B * 4)); }
+
+int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int interleaved, int page_size, int num_pages,
+                    int max_pages, int max_pos, const void* k, long long k_stride, const void* v, long long v_stride,
+                    const void* q, long long q_stride, int dtype, const float* cos_sin, const int32_t* new_lens,
+                    const int32_t* block_table, const int32_t* seq_lens, int32_t* seq_lens_out, void* k_pages,
+                    void* v_pages, void* q_out, void* workspace, size_t workspace_bytes, int32_t* err, void* stream) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 1 || num_pages < 0 || max_pages < 0 || max_pos < 0) return WSVD_ERR_INVALID_ARG;
+  if (B == 0) return WSVD_OK;
+  if (dtype != WSVD_DTYPE_FP16 && dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > Hd) return WSVD_ERR_INVALID_ARG;
+  if (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256) return WSVD_ERR_UNSUPPORTED;
+  if (rot_dim % 16) return WSVD_ERR_UNSUPPORTED;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || B > 65535) return WSVD_ERR_UNSUPPORTED;
+  if ((long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
+  if (!block_table || !seq_lens || !seq_lens_out || !k_pages || !v_pages || !workspace) return WSVD_ERR_INVALID_ARG;
+  if (T > 0 && (!k || !v || (Hq > 0 && (!q || !q_out)))) return WSVD_ERR_INVALID_ARG;
+  if (rot_dim > 0 && !cos_sin) return WSVD_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(k_pages) ||
+      !aligned16(v_pages) || !aligned16(cos_sin) || !aligned16(workspace))
+    return WSVD_ERR_INVALID_ARG;
+  if (k_stride < (long long)Hkv * Hd || v_stride < (long long)Hkv * Hd || k_stride % 8 || v_stride % 8 ||
+      (Hq > 0 && (q_stride < (long long)Hq * Hd || q_stride % 8)))
+    return WSVD_ERR_INVALID_ARG;
+  // Nothing that is written may share a byte with what is read, but for the
+  // two that may be updated in place: the lengths, and a dense q.
+  const size_t tok = (size_t)B * T, pool = ((size_t)num_pages * Hkv << shift) * Hd * 2;
+  auto span = [&](long long stride, int heads) {
+    return tok && heads ? ((tok - 1) * (size_t)stride + (size_t)heads * Hd) * 2 : 0;
+  };
+  const size_t kb = span(k_stride, Hkv), vb = span(v_stride, Hkv), qb = span(q_stride, Hq), ob = tok * Hq * Hd * 2;
+  const size_t tb = (size_t)B * max_pages * 4, cb = (size_t)max_pos * rot_dim * 4, lb = (size_t)B * 4;
+  const bool q_in_place = q_out == q && q_stride == (long long)Hq * Hd;
+  struct Span { const void* p; size_t n; } written[] = {{k_pages, pool}, {v_pages, pool}, {q_out, ob}, {seq_lens_out, lb}};
+  const Span read[] = {{k, kb}, {v, vb}, {q, qb}, {block_table, tb}, {rot_dim ? cos_sin : nullptr, cb},
+                       {new_lens, new_lens ? lb : 0}, {seq_lens, lb}};
+  for (const Span& w : written)
+    for (const Span& r : read) {
+      if (!overlap(w.p, w.n, r.p, r.n)) continue;
+      if ((w.p == q_out && r.p == q && q_in_place) || (w.p == seq_lens_out && r.p == seq_lens && w.p == r.p)) continue;
+      return WSVD_ERR_INVALID_ARG;
+    }
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(written[i].p, written[i].n, written[j].p, written[j].n)) return WSVD_ERR_INVALID_ARG;
+  if (workspace_bytes < paged_kv_append_workspace_size(B)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+
+  KvAppendArgs a{};
+  a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.Hd = Hd; a.rot = rot_dim; a.inter = interleaved != 0;
+  a.page_shift = shift; a.num_pages = num_pages; a.max_pages = max_pages;
+  a.cap = max_pages << shift;
+  if (rot_dim > 0) a.cap = std::min(a.cap, max_pos);
+  a.k = static_cast<const uint16_t*>(k); a.v = static_cast<const uint16_t*>(v); a.q = static_cast<const uint16_t*>(q);
+  a.k_stride = k_stride; a.v_stride = v_stride; a.q_stride = q_stride;
+  a.cos_sin = cos_sin; a.new_lens = new_lens; a.block_table = block_table;
+  a.seq_lens = seq_lens; a.seq_lens_out = seq_lens_out;
+  a.k_pages = static_cast<uint16_t*>(k_pages); a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.counters = static_cast<int32_t*>(workspace); a.err = err;
+  // Enough CTAs to fill the SMs several times, at most 16 tokens in each.
+  a.tokens = (int)std::max<size_t>(1, std::min<size_t>(16, tok / (148 * 8)));
+  const dim3 grid((unsigned)std::max(1, (T + a.tokens - 1) / a.tokens), (unsigned)B);
+  (void)cudaGetLastError();
+  if (dtype == WSVD_DTYPE_BF16) kv_append_kernel<true><<<grid, kAppendCta, 0, as_stream(stream)>>>(a);
+  else kv_append_kernel<false><<<grid, kAppendCta, 0, as_stream(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+}
+
+size_t paged_decode_workspace_size(int B, int Tq, int Hq, int Hkv, int Hd) {
+  if (B < 0 || Tq < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || Hd < 1) return 0;
+  return decode_ws(B, Tq, Hq, Hkv, Hd).total;
+}
+
+int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size, int num_pages, int max_pages,
+                           const int32_t* seq_lens, const int32_t* block_table, const void* q, const void* k_pages,
+                           const void* v_pages, int dtype, float softmax_scale, float* out, void* workspace,
+                           size_t workspace_bytes, int32_t* err, void* stream) {
+  if (B < 0 || Tq < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || num_pages < 0 || max_pages < 0) return WSVD_ERR_INVALID_ARG;
+  if (B == 0) return WSVD_OK;
+  if (dtype != WSVD_DTYPE_FP16 && dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
+  if (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256) return WSVD_ERR_UNSUPPORTED;
+  const int shift = page_shift_of(page_size);
+  const long long nq = (long long)(Hq / Hkv) * Tq;
+  if (shift < 0 || B > 65535 || nq > 64) return WSVD_ERR_UNSUPPORTED;
+  if ((long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
+  if (!seq_lens || !block_table || !q || !k_pages || !v_pages || !out || !workspace) return WSVD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
+    return WSVD_ERR_INVALID_ARG;
+  const DecodeWs ws = decode_ws(B, Tq, Hq, Hkv, Hd);
+  if (workspace_bytes < ws.total) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  const int qc = chunk_queries((int)nq, Hd);
+  const DecodeKernel kern = dtype == WSVD_DTYPE_BF16 ? pick_decode<true>(Hd, qc) : pick_decode<false>(Hd, qc);
+  KvDecodeArgs a{};
+  a.B = B; a.Tq = Tq; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.nq = (int)nq; a.chunks = (int)((nq + qc - 1) / qc);
+  a.page_shift = shift; a.num_pages = num_pages; a.max_pages = max_pages; a.cap = max_pages << shift;
+  a.seq_lens = seq_lens; a.block_table = block_table;
+  a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k_pages);
+  a.v = static_cast<const uint16_t*>(v_pages);
+  a.out = out;
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.partials);
+  a.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + ws.counters);
+  a.err = err;
+  a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
+  (void)cudaGetLastError();
+  if (resident_ctas(kern, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
+  kern.fn<<<a.ctas, kern.threads, kern.smem, as_stream(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+}
+
+}  // extern "C"
