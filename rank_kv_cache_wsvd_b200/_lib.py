@@ -378,7 +378,8 @@ class _Device:
         return None if err is None else self.dense(err, torch.int32, err.shape, "err")
 
     def stream(self):
-        return (self._stream or torch.cuda.current_stream()).cuda_stream
+        # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us a call
+        return self._stream.cuda_stream if self._stream is not None else torch._C._cuda_getCurrentRawStream(self.index)
 
 
 def paged_kv_append_workspace_size(B) -> int:

@@ -182,21 +182,33 @@ __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArg
 // The products cost less than the rows' bytes for up to 16 queries.
 template <bool BF16, int HD, int NB>
 struct DecCfg {
-  static constexpr int kWarps = 4;
+  #ifndef KV_WARPS
+#define KV_WARPS (HD == 256 ? 4 : 8)
+#endif
+#ifndef KV_STAGES
+#define KV_STAGES 3
+#endif
+#ifndef KV_MINB
+#define KV_MINB 1
+#endif
+  static constexpr int kWarps = KV_WARPS;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTS = HD >= 128 ? 16 : (HD == 64 ? 32 : 64);  // rows per strip
   static constexpr int kMT = kTS / 16;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = KV_STAGES;
   static constexpr int kHalf = kTS * HD * 2;      // bytes of a strip's K (or V)
   static constexpr int kStage = 2 * kHalf;
 
   static constexpr int kChunks = HD / 8;          // 16-byte chunks of a row
   static constexpr int kParts = BF16 ? 3 : 2;
   static constexpr int kQ = 8 * NB;               // queries of a chunk
-  static constexpr int kPitch = HD + 4;           // floats per query in the merge scratch
   static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
-  static_assert(kPitch * 8 * 4 <= kStage, "a warp's merge scratch is one stage");
+  static_assert(kQ * HD * 4 <= kStage, "a warp's merge scratch is one stage");
 };
+
+// Floats of one partial result: O [queries][Hd], then (m, l) per query, a
+// multiple of four so that every O row can be read in 16-byte pieces.
+__host__ __device__ constexpr int partial_floats(int queries, int Hd) { return queries * Hd + (2 * queries + 3) / 4 * 4; }
 
 struct KvDecodeArgs {
   int B, Tq, Hq, Hkv, G, nq, chunks, page_shift, num_pages, max_pages, cap, ctas;
@@ -204,7 +216,7 @@ struct KvDecodeArgs {
   const int32_t* block_table;
   const uint16_t *q, *k, *v;
   float* out;
-  float* partials;  // [2 * ctas][min(nq, kQ)][HD + 2]
+  float* partials;  // [2 * ctas] of O [min(nq, kQ)][HD], then (m, l) per query
   int32_t* counters;
   int32_t* err;
   float qscale;
@@ -285,25 +297,24 @@ struct Segment {
 };
 
 template <bool BF16, int HD, int NB>
-__global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
+__global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && NB == 1 ? KV_MINB : 1) kv_decode_kernel(const KvDecodeArgs a) {
   using C = DecCfg<BF16, HD, NB>;
   constexpr int TS = C::kTS, MT = C::kMT, S = C::kStages, NW = C::kWarps, KS = HD / 16, NP = C::kParts;
   // 2^bias keeps the low fp16 part of small weights out of the denormals.
   constexpr float kBias = BF16 ? 0.f : 12.f;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ long long scan[NW];
-  __shared__ int start_b;
-  __shared__ long long start_rem;
   __shared__ float sm_m[NW][C::kQ], sm_l[NW][C::kQ];
   __shared__ int sm_valid[NW][S];
-  __shared__ int sm_last;
+  __shared__ int sm_slot[NW], sm_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
   const int c = blockIdx.x, units = a.Hkv * a.chunks;
 
-  // The strips of all sequences, and where this CTA's share starts.
-  const int per = (a.B + C::kThreads - 1) / C::kThreads;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  // The strips of all sequences, and where this CTA's share starts: every warp
+  // finds it for itself.
+  const int per = (a.B + 31) / 32;
+  const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
   long long sum = 0;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) {
     const int raw = a.seq_lens[b];
     if ((raw < 0 || raw > a.cap) && c == 0) set_err(a.err, WSVD_DEVERR_LEN_RANGE);
@@ -315,14 +326,7 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
     const long long v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = incl - sum;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
+  const long long total = __shfl_sync(0xffffffffu, incl, 31), before = incl - sum;
   const long long G = total * units;
   // Sequences without rows: zeros, spread over the CTAs.
   for (int b = c; b < a.B; b += gridDim.x)
@@ -332,25 +336,30 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
   const long long most = (G + NW - 1) / NW;
   const int CW = (int)(most < a.ctas ? most : a.ctas);
   if (c >= CW) return;
-  const long long g_begin = G * c / CW, g_end = G * (c + 1) / CW;
-  if (g_begin >= before * units && g_begin < (before + sum) * units) {
-    long long rem = g_begin - before * units;
-    int b = b0;
-    for (;; ++b) {
-      const long long ns = (long long)((valid_len(a, b) + TS - 1) / TS) * units;
+  // The first `extra` CTAs take one strip more than the others.
+  const unsigned long long uG = (unsigned long long)G;
+  const long long base = uG < 0x80000000ull ? (uint32_t)G / (uint32_t)CW : G / CW, extra = G - base * CW;
+  const long long g_begin = base * c + min((long long)c, extra), g_end = g_begin + base + (c < extra ? 1 : 0);
+  auto cta_of = [&](long long strip) {  // whose share holds a strip
+    const long long big = extra * (base + 1);
+    return (int)(strip < big ? strip / (base + 1) : extra + (strip - big) / base);
+  };
+  const bool mine = g_begin >= before * units && g_begin < (before + sum) * units;
+  long long rem = g_begin - before * units;
+  int sb = b0;
+  if (mine)
+    for (;; ++sb) {
+      const long long ns = (long long)((valid_len(a, sb) + TS - 1) / TS) * units;
       if (rem < ns) break;
       rem -= ns;
     }
-    start_b = b;
-    start_rem = rem;
-  }
-  __syncthreads();
-
+  const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
   Segment<TS> seg;
-  seg.b = start_b;
+  seg.b = __shfl_sync(0xffffffffu, sb, src);
+  rem = __shfl_sync(0xffffffffu, rem, src);
   seg.n = valid_len(a, seg.b);
-  seg.u = (int)(start_rem / seg.strips());
-  seg.s = (int)(start_rem % seg.strips());
+  seg.u = (int)(rem / seg.strips());
+  seg.s = (int)(rem % seg.strips());
   seg.left = g_end - g_begin;
   seg.e = (int)min((long long)seg.strips(), seg.s + seg.left);
 
@@ -478,7 +487,6 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
       }
       // Running maximum and sum; columns (queries) of sc and o are the same.
       uint32_t pf[MT][NB][NP][2];
-      bool moved = false;
       float alpha[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -492,7 +500,6 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
           const float mn = fmaxf(m[nb][i], mx);
           const float ref = mn == kNegInf ? 0.f : mn;
           alpha[nb][i] = ex2(m[nb][i] - ref);
-          moved |= mn != m[nb][i];
           m[nb][i] = mn;
           float add = 0.f;
 #pragma unroll
@@ -505,14 +512,6 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
             }
           l[nb][i] = l[nb][i] * alpha[nb][i] + add;
         }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int d = 0; d < KS; ++d)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[d][nb][i] *= alpha[nb][i & 1];
-      }
       // A later token's value may be infinite or NaN; it must not reach the
       // queries that do not see it (0 * NaN), so such a strip is summed row by
       // row.  Rows past the length are zero already.
@@ -528,6 +527,12 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
         wild = __any_sync(0xffffffffu, wild);
       }
       if (wild) {
+#pragma unroll
+        for (int d = 0; d < KS; ++d)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][nb][i] *= alpha[nb][i & 1];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll 1
@@ -572,24 +577,38 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
               r0 -= fx.x; r1 -= fx.y; r2 -= fy.x; r3 -= fy.y;
             }
           }
+        // Each strip's product starts at zero and joins O in fp32: the tensor
+        // cores' own sums do not round to nearest, and over a long cache that
+        // bias would show (3e-6 of the output at 32768 rows, 4e-7 this way).
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int d = 0; d < KS; ++d) {
+          float part[NB][4];
 #pragma unroll
-          for (int d = 0; d < KS; ++d) {
+          for (int nb = 0; nb < NB; ++nb) part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.f;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
             uint32_t vf[4];
             ldsm4_t(vf, vb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * d + ((lane >> 3) & 1)));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int k = 0; k < NP; ++k) mma16816<BF16>(o[d][nb], vf, pf[t][nb][k][0], pf[t][nb][k][1]);
+              for (int k = 0; k < NP; ++k) mma16816<BF16>(part[nb], vf, pf[t][nb][k][0], pf[t][nb][k][1]);
           }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][nb][i] = fmaf(o[d][nb][i], alpha[nb][i & 1], part[nb][i]);
+        }
       }
       __syncwarp();  // every lane has read this stage before it is filled again
       last_stage = stage;
       stage = stage == S - 1 ? 0 : stage + 1;
     }
 
-    // ---- the warps' results of this segment: m, l and O joined
+    // ---- the warps' results of this segment, joined.  Each warp leaves O in
+    // its free stage, [query][dim] with bits 3 and 4 of dim turned by the lane
+    // so that the stores meet no bank twice and float4 reads stay whole.
+    float* scratch = reinterpret_cast<float*>(ring) + (size_t)(warp * S + last_stage) * (C::kStage / 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -597,98 +616,111 @@ __global__ void __launch_bounds__(128) kv_decode_kernel(const KvDecodeArgs a) {
         float v = l[nb][i];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        const int j = nb * 8 + 2 * c4 + i;
         if (g == 0) {
-          sm_m[warp][nb * 8 + 2 * c4 + i] = m[nb][i];
-          sm_l[warp][nb * 8 + 2 * c4 + i] = v;
+          sm_m[warp][j] = m[nb][i];
+          sm_l[warp][j] = v;
+        }
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+          scratch[j * HD + ((d * 16 + g) ^ (c4 << 3))] = o[d][nb][i];
+          scratch[j * HD + ((d * 16 + 8 + g) ^ (c4 << 3))] = o[d][nb][2 + i];
         }
       }
+    if (lane == 0) sm_slot[warp] = warp * S + last_stage;
     __syncthreads();
     const int ns = seg.strips();
     const bool whole = seg.s == 0 && seg.e == ns;
     const int qmax = min(C::kQ, a.nq);  // queries per partial slot
-    float* part = a.partials + (size_t)(2 * c + (first_segment ? 0 : 1)) * qmax * (HD + 2);
-    float* scratch = reinterpret_cast<float*>(ring);
-    const uint32_t my_scratch = (uint32_t)(warp * S + last_stage) * (C::kStage / 4);
-    __shared__ int sm_slot[NW];
-    if (lane == 0) sm_slot[warp] = warp * S + last_stage;
+    const int slot = partial_floats(qmax, HD);
+    float* part = a.partials + (size_t)(2 * c + (first_segment ? 0 : 1)) * slot;
+    auto store = [&](int j, int d, float4 v, float L) {
+      const int jq = j0 + j, t = jq / a.G;
+      const float f = lim_min + t > 0 ? 1.f / L : 0.f;
+      if (f == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(a.out + (((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d) =
+          make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    };
+    for (int idx = tid; idx < nq * (HD / 4); idx += C::kThreads) {
+      const int j = idx / (HD / 4), d = idx % (HD / 4) * 4;
+      float M = kNegInf, L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      if (nb * 8 >= nq) break;
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w][j]);
+      const float ref = M == kNegInf ? 0.f : M;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int j = nb * 8 + 2 * c4 + i;
-        float M = kNegInf;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w][j]);
-        const float f = ex2(m[nb][i] - (M == kNegInf ? 0.f : M));
-#pragma unroll
-        for (int d = 0; d < KS; ++d) {
-          scratch[my_scratch + (2 * c4 + i) * C::kPitch + d * 16 + g] = o[d][nb][i] * f;
-          scratch[my_scratch + (2 * c4 + i) * C::kPitch + d * 16 + 8 + g] = o[d][nb][2 + i] * f;
-        }
+      for (int w = 0; w < NW; ++w) {
+        const float f = ex2(sm_m[w][j] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring) +
+                                                          (size_t)sm_slot[w] * (C::kStage / 4) + j * HD +
+                                                          (d ^ (((j >> 1) & 3) << 3)));
+        L = fmaf(sm_l[w][j], f, L);
+        v.x = fmaf(x.x, f, v.x);
+        v.y = fmaf(x.y, f, v.y);
+        v.z = fmaf(x.z, f, v.z);
+        v.w = fmaf(x.w, f, v.w);
       }
-      __syncthreads();
-      const int here = min(8, nq - nb * 8);
-      for (int idx = tid; idx < here * HD; idx += C::kThreads) {
-        const int jj = idx / HD, d = idx % HD, j = nb * 8 + jj;
-        float M = kNegInf, L = 0.f, sumo = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w][j]);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          L += sm_l[w][j] * ex2(sm_m[w][j] - (M == kNegInf ? 0.f : M));
-          sumo += scratch[(size_t)sm_slot[w] * (C::kStage / 4) + jj * C::kPitch + d];
-        }
-        if (whole) {
-          const int jq = j0 + j, t = jq / a.G;
-          a.out[(((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d] =
-              lim_min + t > 0 ? sumo / L : 0.f;
-        } else {
-          part[j * (HD + 2) + 2 + d] = sumo;
-          if (d == 0) {
-            part[j * (HD + 2)] = M;
-            part[j * (HD + 2) + 1] = L;
-          }
-        }
+      if (whole) {
+        store(j, d, v, L);
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + j * HD + d), v);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + qmax * HD + 2 * j), make_float2(M, L));
       }
-      __syncthreads();
     }
 
     // ---- a unit cut over several CTAs: the last to arrive joins the partials
     // in the order of the CTAs, so the result does not depend on who that is.
     if (!whole) {
-      const long long u0 = g_end - seg.left - seg.s, u1 = u0 + ns;  // the unit's strips in the whole order
-      const int cf = (int)(((u0 + 1) * CW - 1) / G), cl = (int)((u1 * CW - 1) / G);
+      const long long u0 = g_end - seg.left - seg.s;  // the unit's first strip in the whole order
+      const int cf = cta_of(u0), np = cta_of(u0 + ns - 1) - cf + 1;
       const size_t unit = (size_t)seg.b * units + seg.u;
       __threadfence();
       __syncthreads();
-      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + unit, 1) == cl - cf;
+      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + unit, 1) == np - 1;
       __syncthreads();
       if (sm_last) {
         __threadfence();
-        // the unit is the first segment of every CTA but perhaps the first one
-        const bool cf_first = G * cf / CW == u0;
-        const size_t slot = (size_t)qmax * (HD + 2);
-        for (int idx = tid; idx < nq * HD; idx += C::kThreads) {
-          const int j = idx / HD, d = idx % HD;
-          float M = kNegInf, L = 0.f, sumo = 0.f;
-          for (int cc = cf; cc <= cl; ++cc) {
-            const float* p = a.partials + (size_t)(2 * cc + (cc > cf || cf_first ? 0 : 1)) * slot + j * (HD + 2);
-            M = fmaxf(M, __ldcg(p));
+        // The unit is the first segment of each of these CTAs, but perhaps of the first.
+        const int skip = base * cf + min((long long)cf, extra) == u0 ? 0 : slot;
+        const float* from = a.partials + (size_t)2 * cf * slot;
+        constexpr int kJoin = 8;  // partials whose loads are in flight together
+        for (int idx = tid; idx < nq * (HD / 4); idx += C::kThreads) {
+          const int j = idx / (HD / 4), d = idx % (HD / 4) * 4;
+          float M = kNegInf, L = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i0 = 0; i0 < np; i0 += kJoin) {
+            float2 ml[kJoin];
+            float4 x[kJoin];
+            float top = M;
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {
+              const float* p = from + (size_t)2 * (i0 + i) * slot + (i0 + i == 0 ? skip : 0);
+              const bool in = i0 + i < np;
+              ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + qmax * HD + 2 * j)) : make_float2(kNegInf, 0.f);
+              x[i] = in ? __ldcg(reinterpret_cast<const float4*>(p + j * HD + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) top = fmaxf(top, ml[i].x);
+            const float ref = top == kNegInf ? 0.f : top, f0 = ex2(M - ref);
+            L *= f0;
+            v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {
+              const float f = ex2(ml[i].x - ref);
+              L = fmaf(ml[i].y, f, L);
+              v.x = fmaf(x[i].x, f, v.x);
+              v.y = fmaf(x[i].y, f, v.y);
+              v.z = fmaf(x[i].z, f, v.z);
+              v.w = fmaf(x[i].w, f, v.w);
+            }
+            M = top;
           }
-          for (int cc = cf; cc <= cl; ++cc) {
-            const float* p = a.partials + (size_t)(2 * cc + (cc > cf || cf_first ? 0 : 1)) * slot + j * (HD + 2);
-            const float f = ex2(__ldcg(p) - (M == kNegInf ? 0.f : M));
-            L = fmaf(__ldcg(p + 1), f, L);
-            sumo = fmaf(__ldcg(p + 2 + d), f, sumo);
-          }
-          const int jq = j0 + j, t = jq / a.G;
-          a.out[(((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d] =
-              lim_min + t > 0 ? sumo / L : 0.f;
+          store(j, d, v, L);
         }
         if (tid == 0) st_relaxed_gpu(a.counters + unit, 0);
       }
     }
+    __syncthreads();  // the scratch and the statistics are free again
     go = seg.next(a);
     first_segment = false;
   }
@@ -769,7 +801,7 @@ DecodeWs decode_ws(int B, int Tq, int Hq, int Hkv, int Hd) {
   const int nq = Hq / Hkv * Tq, qc = chunk_queries(nq, Hd), chunks = (nq + qc - 1) / qc;
   DecodeWs w;
   w.partials = 0;
-  w.counters = align16((size_t)2 * kMaxPagedCtas * std::min(nq, qc) * (Hd + 2) * sizeof(float));
+  w.counters = align16((size_t)2 * kMaxPagedCtas * partial_floats(std::min(nq, qc), Hd) * sizeof(float));
   w.total = w.counters + align16((size_t)B * Hkv * chunks * sizeof(int32_t));
   return w;
 }
