@@ -309,77 +309,67 @@ def shared_latent_svd_decode(q, lat_k, lat_v, B_k, B_v, seq_lens, softmax_scale:
 
 
 # ----------------------------------------------------------------------------- paged dense cache
-class _Device:
-    """The device that every tensor of a call lies on, made current for the call
-    (the library launches on the current device) when another one is."""
-
-    def __init__(self, t, stream=None):
-        if not t.is_cuda:
-            raise WsvdError("all tensors must be CUDA tensors")
-        self.index = t.get_device()
-        if stream is not None and stream.device_index != self.index:
-            raise WsvdError(f"stream: expected one of cuda:{self.index}, got one of cuda:{stream.device_index}")
-        self._stream = stream
-        self._back = torch.cuda.current_device()
-
-    def __enter__(self):
-        if self.index != self._back:
-            torch.cuda.set_device(self.index)
-        return self
-
-    def __exit__(self, *exc):
-        if self.index != self._back:
-            torch.cuda.set_device(self._back)
-
-    def new(self, make, shape, dtype):
-        """A tensor made on the call's stream, so that its memory and its fill
-        are ordered with the launch."""
-        if self._stream is None:
-            return make(shape, dtype=dtype, device="cuda")
-        with torch.cuda.stream(self._stream):
-            return make(shape, dtype=dtype, device="cuda")
-
-    def dense(self, t, dtype, shape, name):
-        """Address of a dense tensor of this device with the dtype and shape given."""
-        if t.dtype != dtype or t.shape != shape:
-            raise WsvdError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if t.get_device() != self.index:
-            raise WsvdError(f"{name}: expected a tensor on cuda:{self.index}, got {t.device}")
-        if not t.is_contiguous():
-            raise WsvdError(f"{name} must be contiguous")
+# The calls below check all their arguments but are written flat: at the sizes
+# of one decode step a call's host time is what a caller waits for.
+def _dense(t, dtype, shape, index, name):
+    """Address of a dense tensor on cuda:index with the dtype and shape given."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
+    if not t.is_cuda:
+        raise WsvdError("all tensors must be CUDA tensors")
+    _expect(t, dtype, shape, name)
+    if t.get_device() != index:
+        raise WsvdError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
+    raise WsvdError(f"{name} must be contiguous")
 
-    def tokens(self, t, dtype, shape, name):
-        """Address and token stride of [B][T][heads][Hd] whose heads are dense and
-        whose batch and token axes step as one (a slice of a fused projection)."""
-        if t.dtype != dtype or t.shape != shape:
-            raise WsvdError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if t.get_device() != self.index:
-            raise WsvdError(f"{name}: expected a tensor on cuda:{self.index}, got {t.device}")
-        B, T, heads, Hd = shape
-        sb, st, sh, sd = t.stride()
-        if T == 1:
-            st = sb if B > 1 else heads * Hd
-        if t.numel() and (sd != 1 or (heads > 1 and sh != Hd) or (B > 1 and sb != T * st)):
-            raise WsvdError(f"{name}: the heads of a token must be dense and tokens evenly spaced, "
-                            f"got strides {tuple(t.stride())}")
-        return t.data_ptr(), st if t.numel() else heads * Hd
 
-    def optional(self, t, dtype, shape, name):
-        return None if t is None else self.dense(t, dtype, shape, name)
+def _tokens(t, dtype, shape, index, name):
+    """Address and token stride of [B][T][heads][Hd] whose heads are dense and
+    whose batch and token axes step as one (a slice of a fused projection)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        return _dense(t, dtype, shape, index, name), 0  # raises
+    B, T, heads, Hd = shape
+    sb, st, sh, sd = t.stride()
+    if T == 1:
+        st = sb if B > 1 else heads * Hd
+    if B * T == 0:
+        return t.data_ptr(), heads * Hd
+    if sd != 1 or (heads > 1 and sh != Hd) or (B > 1 and sb != T * st):
+        raise WsvdError(f"{name}: the heads of a token must be dense and tokens evenly spaced, got strides {t.stride()}")
+    return t.data_ptr(), st
 
-    def scratch(self, t, nbytes):
-        """Address and bytes of the caller's workspace, or of a new zeroed one."""
-        if t is None:
-            t = self.new(torch.zeros, (max(16, nbytes),), torch.uint8)
-        return self.dense(t, torch.uint8, t.shape, "workspace_buf"), t.numel(), t
 
-    def error_word(self, err):
-        return None if err is None else self.dense(err, torch.int32, err.shape, "err")
+def _new(make, shape, dtype, index, stream):
+    """A tensor made on the call's stream, so that its memory and its fill are
+    ordered with the launch."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=f"cuda:{index}")
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=f"cuda:{index}")
 
-    def stream(self):
-        # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us a call
-        return self._stream.cuda_stream if self._stream is not None else torch._C._cuda_getCurrentRawStream(self.index)
+
+def _scratch(t, index, stream, size_of, *sizes):
+    """The caller's workspace, or a new zeroed one of size_of(*sizes) bytes."""
+    if t is None:
+        return _new(torch.zeros, (max(16, size_of(*sizes)),), torch.uint8, index, stream)
+    _dense(t, torch.uint8, (t.numel(),), index, "workspace_buf")
+    return t
+
+
+def _raw_stream(stream, index):
+    if stream is None:  # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise WsvdError(f"stream: expected one of cuda:{index}, got one of cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
+def _launch(index, fn, *args):
+    """The C call with the tensors' device current (the library launches there)."""
+    if torch.cuda.current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def paged_kv_append_workspace_size(B) -> int:
@@ -402,34 +392,35 @@ def paged_kv_append(k, v, k_pages, v_pages, block_table, seq_lens, q=None, q_out
     B, T, Hkv, Hd = k.shape
     num_pages, _, page_size, _ = k_pages.shape
     max_pages = block_table.shape[1]
-    dtype, code = k.dtype, _dtype_code(k)
-    with _Device(k, stream) as dev:
-        pk, sk = dev.tokens(k, dtype, (B, T, Hkv, Hd), "k")
-        pv, sv = dev.tokens(v, dtype, (B, T, Hkv, Hd), "v")
-        Hq, pq, sq, po = 0, None, 0, None
-        if q is not None:
-            Hq = q.shape[2]
-            pq, sq = dev.tokens(q, dtype, (B, T, Hq, Hd), "q")
-            if q_out is None:
-                q_out = dev.new(torch.empty, (B, T, Hq, Hd), dtype)
-            po = dev.dense(q_out, dtype, (B, T, Hq, Hd), "q_out")
-        elif q_out is not None:
-            raise WsvdError("q_out without q")
-        max_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-        if seq_lens_out is None:
-            seq_lens_out = seq_lens
-        ws, ws_bytes, keep = dev.scratch(workspace_buf, lib.paged_kv_append_workspace_size(B))
-        st = lib.paged_kv_append(
-            B, T, Hq, Hkv, Hd, rot, int(interleaved), page_size, num_pages, max_pages, max_pos, pk, sk, pv, sv, pq, sq,
-            code, dev.optional(cos_sin, torch.float32, (max_pos, rot), "cos_sin"),
-            dev.optional(new_lens, torch.int32, (B,), "new_lens"),
-            dev.dense(block_table, torch.int32, (B, max_pages), "block_table"),
-            dev.dense(seq_lens, torch.int32, (B,), "seq_lens"),
-            dev.dense(seq_lens_out, torch.int32, (B,), "seq_lens_out"),
-            dev.dense(k_pages, dtype, (num_pages, Hkv, page_size, Hd), "k_pages"),
-            dev.dense(v_pages, dtype, (num_pages, Hkv, page_size, Hd), "v_pages"), po, ws, ws_bytes,
-            dev.error_word(err), dev.stream())
-    _check(st, "paged_kv_append")
+    dtype, dev, i32 = k.dtype, k.get_device(), torch.int32
+    code = _dtype_code(k)
+    pk, sk = _tokens(k, dtype, (B, T, Hkv, Hd), dev, "k")
+    pv, sv = _tokens(v, dtype, (B, T, Hkv, Hd), dev, "v")
+    Hq, pq, sq, po = 0, None, 0, None
+    if q is not None:
+        Hq = q.shape[2]
+        pq, sq = _tokens(q, dtype, (B, T, Hq, Hd), dev, "q")
+        if q_out is None:
+            q_out = _new(torch.empty, (B, T, Hq, Hd), dtype, dev, stream)
+        po = _dense(q_out, dtype, (B, T, Hq, Hd), dev, "q_out")
+    elif q_out is not None:
+        raise WsvdError("q_out without q")
+    max_pos, rot, pc = 0, 0, None
+    if cos_sin is not None:
+        max_pos, rot = cos_sin.shape
+        pc = _dense(cos_sin, torch.float32, (max_pos, rot), dev, "cos_sin")
+    pn = None if new_lens is None else _dense(new_lens, i32, (B,), dev, "new_lens")
+    pl = _dense(seq_lens, i32, (B,), dev, "seq_lens")
+    plo = pl if seq_lens_out is None else _dense(seq_lens_out, i32, (B,), dev, "seq_lens_out")
+    pages = (num_pages, Hkv, page_size, Hd)
+    ws = _scratch(workspace_buf, dev, stream, lib.paged_kv_append_workspace_size, B)
+    st = _launch(dev, lib.paged_kv_append, B, T, Hq, Hkv, Hd, rot, interleaved, page_size, num_pages, max_pages, max_pos,
+                 pk, sk, pv, sv, pq, sq, code, pc, pn, _dense(block_table, i32, (B, max_pages), dev, "block_table"), pl,
+                 plo, _dense(k_pages, dtype, pages, dev, "k_pages"), _dense(v_pages, dtype, pages, dev, "v_pages"), po,
+                 ws.data_ptr(), ws.numel(), None if err is None else _dense(err, i32, err.shape, dev, "err"),
+                 _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_kv_append")
     return q_out
 
 
@@ -439,25 +430,28 @@ def paged_decode_attention(q, k_pages, v_pages, block_table, seq_lens, softmax_s
     over k_pages, v_pages [num_pages][Hkv][page_size][Hd]; query token t sees
     rows [0, seq_lens[b] - Tq + 1 + t).  Returns out, fp32, in q's shape."""
     lib = load()
-    if q.dim() == 4:
-        B, Tq, Hq, Hd = q.shape
+    shape = q.shape
+    if len(shape) == 4:
+        B, Tq, Hq, Hd = shape
     else:
-        B, Hq, Hd = q.shape
+        B, Hq, Hd = shape
         Tq = 1
     num_pages, Hkv, page_size, _ = k_pages.shape
     max_pages = block_table.shape[1]
-    dtype, code = q.dtype, _dtype_code(q)
-    with _Device(q, stream) as dev:
-        if out is None:
-            out = dev.new(torch.empty, q.shape, torch.float32)
-        ws, ws_bytes, keep = dev.scratch(workspace_buf, lib.paged_decode_workspace_size(B, Tq, Hq, Hkv, Hd))
-        st = lib.paged_decode_attention(
-            B, Tq, Hq, Hkv, Hd, page_size, num_pages, max_pages, dev.dense(seq_lens, torch.int32, (B,), "seq_lens"),
-            dev.dense(block_table, torch.int32, (B, max_pages), "block_table"), dev.dense(q, dtype, q.shape, "q"),
-            dev.dense(k_pages, dtype, (num_pages, Hkv, page_size, Hd), "k_pages"),
-            dev.dense(v_pages, dtype, (num_pages, Hkv, page_size, Hd), "v_pages"), code, softmax_scale,
-            dev.dense(out, torch.float32, q.shape, "out"), ws, ws_bytes, dev.error_word(err), dev.stream())
-    _check(st, "paged_decode_attention")
+    dtype, dev = q.dtype, q.get_device()
+    code = _dtype_code(q)
+    if out is None:
+        out = _new(torch.empty, shape, torch.float32, dev, stream)
+    pages = (num_pages, Hkv, page_size, Hd)
+    ws = _scratch(workspace_buf, dev, stream, lib.paged_decode_workspace_size, B, Tq, Hq, Hkv, Hd)
+    st = _launch(dev, lib.paged_decode_attention, B, Tq, Hq, Hkv, Hd, page_size, num_pages, max_pages,
+                 _dense(seq_lens, torch.int32, (B,), dev, "seq_lens"),
+                 _dense(block_table, torch.int32, (B, max_pages), dev, "block_table"), _dense(q, dtype, shape, dev, "q"),
+                 _dense(k_pages, dtype, pages, dev, "k_pages"), _dense(v_pages, dtype, pages, dev, "v_pages"), code,
+                 softmax_scale, _dense(out, torch.float32, shape, dev, "out"), ws.data_ptr(), ws.numel(),
+                 None if err is None else _dense(err, torch.int32, err.shape, dev, "err"), _raw_stream(stream, dev))
+    if st:
+        _check(st, "paged_decode_attention")
     return out
 
 

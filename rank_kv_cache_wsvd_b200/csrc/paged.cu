@@ -182,23 +182,21 @@ __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArg
 // The products cost less than the rows' bytes for up to 16 queries.
 template <bool BF16, int HD, int NB>
 struct DecCfg {
-  #ifndef KV_WARPS
-#define KV_WARPS (HD == 256 ? 4 : 8)
-#endif
-#ifndef KV_STAGES
-#define KV_STAGES 3
-#endif
-#ifndef KV_MINB
-#define KV_MINB 1
-#endif
-  static constexpr int kWarps = KV_WARPS;
+  // Rows per strip, warps per CTA and stages per warp: strips of 8 KB (16 KB at
+  // head size 256), 192 KB of them per SM.  Twelve warps of two stages beat
+  // eight of three (4 x 32768 rows of 8 heads of 128: 84.7 us against 87.3; 64
+  // with 16 queries a head, 9 x 32768 rows: 56.6 against 63.4) except where two
+  // column blocks of head size 128 leave registers for eight warps only (twelve,
+  // spilling: 109.3 against 107.3).  Strips of half the size need more warps for
+  // the same bytes and lose (64, sixteen warps of three: 66.0).
+  static constexpr bool kWide = HD == 128 && NB == 2;
+  static constexpr int kTS = HD >= 128 ? 16 : (HD == 64 ? 32 : 64);
+  static constexpr int kWarps = HD == 256 ? 6 : kWide ? 8 : 12;
+  static constexpr int kStages = kWide ? 3 : 2;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kTS = HD >= 128 ? 16 : (HD == 64 ? 32 : 64);  // rows per strip
   static constexpr int kMT = kTS / 16;
-  static constexpr int kStages = KV_STAGES;
   static constexpr int kHalf = kTS * HD * 2;      // bytes of a strip's K (or V)
   static constexpr int kStage = 2 * kHalf;
-
   static constexpr int kChunks = HD / 8;          // 16-byte chunks of a row
   static constexpr int kParts = BF16 ? 3 : 2;
   static constexpr int kQ = 8 * NB;               // queries of a chunk
@@ -244,19 +242,19 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t movm_t(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (BF16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -276,28 +274,45 @@ __device__ __forceinline__ int valid_len(const KvDecodeArgs& a, int b) {
   return n < 0 || n > a.cap ? 0 : n;
 }
 
-// A segment: strips [s, e) of unit u (KV head * chunks + chunk) of sequence b.
+// What a segment costs beside its strips (queries, joins), in strips.  A unit
+// counts as its strips plus so many when the CTAs' shares are cut, else a CTA
+// that meets many short sequences would be the last to finish.
+constexpr int kLead = 24;
+
+template <int TS>
+__device__ __forceinline__ int counted(int n) {  // a unit of a sequence with n rows
+  return n > 0 ? (n + TS - 1) / TS + kLead : 0;
+}
+
+// A segment: strips [s, e) of unit u (KV head * chunks + chunk) of sequence b;
+// none when the CTA's share of the unit ends within the lead.
 template <int TS>
 struct Segment {
   int b, u, n, s, e;
-  long long left;  // strips of the CTA's share from s on
+  int at, taken;   // where the CTA's share begins in the unit (lead included), and how much of the unit it takes
+  long long left;  // of the CTA's share from here on
   __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
+  __device__ __forceinline__ void enter(int place) {
+    at = place;
+    taken = (int)min((long long)(strips() + kLead - at), left);
+    s = max(0, at - kLead);
+    e = max(0, at + taken - kLead);
+  }
   __device__ __forceinline__ bool next(const KvDecodeArgs& a) {
-    left -= e - s;
+    left -= taken;
     if (left <= 0) return false;
     if (++u == a.Hkv * a.chunks) {
       u = 0;
       do n = valid_len(a, ++b);
       while (n == 0);
     }
-    s = 0;
-    e = (int)min((long long)strips(), left);
+    enter(0);
     return true;
   }
 };
 
 template <bool BF16, int HD, int NB>
-__global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && NB == 1 ? KV_MINB : 1) kv_decode_kernel(const KvDecodeArgs a) {
+__global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_kernel(const KvDecodeArgs a) {
   using C = DecCfg<BF16, HD, NB>;
   constexpr int TS = C::kTS, MT = C::kMT, S = C::kStages, NW = C::kWarps, KS = HD / 16, NP = C::kParts;
   // 2^bias keeps the low fp16 part of small weights out of the denormals.
@@ -318,7 +333,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
   for (int b = b0; b < b1; ++b) {
     const int raw = a.seq_lens[b];
     if ((raw < 0 || raw > a.cap) && c == 0) set_err(a.err, WSVD_DEVERR_LEN_RANGE);
-    sum += (valid_len(a, b) + TS - 1) / TS;
+    sum += counted<TS>(valid_len(a, b));
   }
   long long incl = sum;
 #pragma unroll
@@ -349,7 +364,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
   int sb = b0;
   if (mine)
     for (;; ++sb) {
-      const long long ns = (long long)((valid_len(a, sb) + TS - 1) / TS) * units;
+      const long long ns = (long long)counted<TS>(valid_len(a, sb)) * units;
       if (rem < ns) break;
       rem -= ns;
     }
@@ -358,10 +373,9 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
   seg.b = __shfl_sync(0xffffffffu, sb, src);
   rem = __shfl_sync(0xffffffffu, rem, src);
   seg.n = valid_len(a, seg.b);
-  seg.u = (int)(rem / seg.strips());
-  seg.s = (int)(rem % seg.strips());
+  seg.u = (int)(rem / (seg.strips() + kLead));
   seg.left = g_end - g_begin;
-  seg.e = (int)min((long long)seg.strips(), seg.s + seg.left);
+  seg.enter((int)(rem % (seg.strips() + kLead)));
 
   // ---- the warp's copies: cursor `ld`, page ids one strip ahead
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
@@ -418,8 +432,8 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
   int stage = 0;  // of the next strip to read
 
   // ---- segment by segment
-  bool first_segment = true;
-  for (bool go = true; go;) {
+  for (bool go = true; go; go = seg.next(a)) {
+    if (seg.s == seg.e) continue;
     const int h = seg.u / a.chunks, j0 = (seg.u % a.chunks) * C::kQ;
     const int nq = min(C::kQ, a.nq - j0);
     uint32_t qf[NB][KS][2];
@@ -453,25 +467,31 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
       __syncwarp();
       issue(stage == 0 ? S - 1 : stage - 1);
       const uint32_t kb = my_ring + (uint32_t)stage * C::kStage, vb = kb + C::kHalf;
-      float sc[MT][NB][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[t][nb][0] = sc[t][nb][1] = sc[t][nb][2] = sc[t][nb][3] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t kf[4];
-          ldsm4(kf, kb + strip_off<HD>(t * 16 + (lane & 15), 2 * k + (lane >> 4)));
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(sc[t][nb], kf, qf[nb][k][0], qf[nb][k][1]);
-        }
-      }
+      // Two sums per column block (even and odd steps of 16 values), so that
+      // consecutive products do not wait for one another.
+      float sc[MT][NB][4], sc2[MT][NB][4];
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[t][nb][i] *= a.qscale;
+          for (int i = 0; i < 4; ++i) sc[t][nb][i] = sc2[t][nb][i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t kf[4];
+          ldsm4(kf, kb + strip_off<HD>(t * 16 + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816<BF16>(k & 1 ? sc2[t][nb] : sc[t][nb], kf, qf[nb][k][0], qf[nb][k][1]);
+        }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][nb][i] = (sc[t][nb][i] + sc2[t][nb][i]) * a.qscale;
       const int l0 = s * TS, valid = sm_valid[warp][stage];
       const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
       if (masked) {
@@ -580,24 +600,35 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
         // Each strip's product starts at zero and joins O in fp32: the tensor
         // cores' own sums do not round to nearest, and over a long cache that
         // bias would show (3e-6 of the output at 32768 rows, 4e-7 this way).
+        // Several dim blocks at a time, for products that do not wait for one another.
+        constexpr int DG = KS < 4 ? KS : 4 / NB;
 #pragma unroll
-        for (int d = 0; d < KS; ++d) {
-          float part[NB][4];
+        for (int d0 = 0; d0 < KS; d0 += DG) {
+          float part[DG][NB][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) part[nb][0] = part[nb][1] = part[nb][2] = part[nb][3] = 0.f;
+          for (int d = 0; d < DG; ++d)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) part[d][nb][0] = part[d][nb][1] = part[d][nb][2] = part[d][nb][3] = 0.f;
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            uint32_t vf[4];
-            ldsm4_t(vf, vb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * d + ((lane >> 3) & 1)));
+            uint32_t vf[DG][4];
+#pragma unroll
+            for (int d = 0; d < DG; ++d)
+              ldsm4_t(vf[d], vb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7),
+                                                2 * (d0 + d) + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+#pragma unroll
+              for (int d = 0; d < DG; ++d)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(part[d][nb], vf[d], pf[t][nb][k][0], pf[t][nb][k][1]);
+          }
+#pragma unroll
+          for (int d = 0; d < DG; ++d)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int k = 0; k < NP; ++k) mma16816<BF16>(part[nb], vf, pf[t][nb][k][0], pf[t][nb][k][1]);
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[d][nb][i] = fmaf(o[d][nb][i], alpha[nb][i & 1], part[nb][i]);
+              for (int i = 0; i < 4; ++i) o[d0 + d][nb][i] = fmaf(o[d0 + d][nb][i], alpha[nb][i & 1], part[d][nb][i]);
         }
       }
       __syncwarp();  // every lane has read this stage before it is filled again
@@ -633,7 +664,8 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
     const bool whole = seg.s == 0 && seg.e == ns;
     const int qmax = min(C::kQ, a.nq);  // queries per partial slot
     const int slot = partial_floats(qmax, HD);
-    float* part = a.partials + (size_t)(2 * c + (first_segment ? 0 : 1)) * slot;
+    // A CTA has at most one unit that it begins within, and one that it only begins.
+    float* part = a.partials + (size_t)(2 * c + (seg.s == 0 ? 1 : 0)) * slot;
     auto store = [&](int j, int d, float4 v, float L) {
       const int jq = j0 + j, t = jq / a.G;
       const float f = lim_min + t > 0 ? 1.f / L : 0.f;
@@ -671,7 +703,8 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
     // ---- a unit cut over several CTAs: the last to arrive joins the partials
     // in the order of the CTAs, so the result does not depend on who that is.
     if (!whole) {
-      const long long u0 = g_end - seg.left - seg.s;  // the unit's first strip in the whole order
+      // the place of the unit's first strip in the whole order
+      const long long u0 = g_end - seg.left - seg.at + kLead;
       const int cf = cta_of(u0), np = cta_of(u0 + ns - 1) - cf + 1;
       const size_t unit = (size_t)seg.b * units + seg.u;
       __threadfence();
@@ -680,8 +713,6 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
       __syncthreads();
       if (sm_last) {
         __threadfence();
-        // The unit is the first segment of each of these CTAs, but perhaps of the first.
-        const int skip = base * cf + min((long long)cf, extra) == u0 ? 0 : slot;
         const float* from = a.partials + (size_t)2 * cf * slot;
         constexpr int kJoin = 8;  // partials whose loads are in flight together
         for (int idx = tid; idx < nq * (HD / 4); idx += C::kThreads) {
@@ -694,7 +725,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
             float top = M;
 #pragma unroll
             for (int i = 0; i < kJoin; ++i) {
-              const float* p = from + (size_t)2 * (i0 + i) * slot + (i0 + i == 0 ? skip : 0);
+              const float* p = from + (size_t)2 * (i0 + i) * slot + (i0 + i == 0 ? slot : 0);  // slot 1 of the first CTA
               const bool in = i0 + i < np;
               ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + qmax * HD + 2 * j)) : make_float2(kNegInf, 0.f);
               x[i] = in ? __ldcg(reinterpret_cast<const float4*>(p + j * HD + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -721,8 +752,6 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, HD <= 128 && N
       }
     }
     __syncthreads();  // the scratch and the statistics are free again
-    go = seg.next(a);
-    first_segment = false;
   }
   cp_wait<0>();
 }
