@@ -20,7 +20,7 @@ namespace {
 // ------------------------------------------------------------------ append
 struct KvAppendArgs {
   int T, Hq, Hkv, Hd, rot, inter, page_shift, num_pages, max_pages, cap;
-  int tokens;  // tokens per CTA
+  int row_slots;  // threads that share a token's rows, per unit (a power of two)
   const uint16_t *k, *v, *q;
   long long k_stride, v_stride, q_stride;
   const float* cos_sin;
@@ -33,7 +33,10 @@ struct KvAppendArgs {
   int32_t* err;
 };
 
-constexpr int kAppendCta = 256;
+// Small CTAs, since each waits out its length and page loads: 8 x 2048 tokens of
+// 32 + 2 x 8 heads of 128 take 64.7 us with 128 threads, 67.5 with 256, 73.5 with
+// 512; 576 tokens of 96 heads 5.8, 7.5 and 12.3 us; one token 3.06, 2.93 and 3.2.
+constexpr int kAppendCta = 128;
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -53,7 +56,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // The rotation of 8 pairs (a_i, b_i): a' = a cos - b sin, b' = b cos + a sin,
 // in fp32, rounded once to the 16-bit type of the cache.  x, y: the two
 // 16-byte chunks of a unit.  Split pairs: a_i in x, b_i in y; interleaved: the
-// pairs lie side by side, four in x, four in y.
+// pairs lie side by side, the first four in x, the others in y.
 template <bool BF16>
 __device__ __forceinline__ void rotate_unit(uint4& x, uint4& y, const float4* cs, const float4* sn, bool inter) {
   uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
@@ -78,14 +81,48 @@ __device__ __forceinline__ void rotate_unit(uint4& x, uint4& y, const float4* cs
   }
 }
 
-// grid (token tiles, B).  A unit is 32 bytes of one head's row: the two 16-byte
-// chunks whose values are rotated together (split pairs: chunks i and
-// i + rot/16), or two neighbouring chunks.
+// grid (token tiles, B).  A unit is 32 bytes of one head's row: 16-byte chunks i
+// and i + rot/16 of the rotated values (which split pairs need together), or
+// two chunks half of the rest apart, so that the threads of a row always touch
+// neighbouring chunks.  A thread keeps one token and one unit, so it reads its
+// cosines and sines and the token's page once, and walks the token's rows (Hq
+// of q, Hkv of k, Hkv of v) kAppendRows at a time, their loads in flight
+// together; the first of them leave before the length and the page table, which
+// they do not depend on, are known.  Bound by the bytes for prompts (8 x 2048
+// tokens, 32 + 2 x 8 heads of 128: 64.7 us, 6.35 TB/s), by three dependent loads
+// (length, page, angle) for one token (3 us).  Six rows at a time: with three the
+// same prompts took 69.6, with four, which leave a part-filled second turn, 82.2.
+constexpr int kAppendRows = 6;
+
 template <bool BF16>
 __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArgs a) {
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int pos = a.seq_lens[b];
+  const int units = a.Hd / 16, rows = a.Hq + 2 * a.Hkv, ru = a.rot / 16;
+  const int unit = tid & (units - 1), slot = tid / units;
+  const int step = a.row_slots, t = blockIdx.x * (kAppendCta / units / step) + slot / step;
+  // A padded block's counts come first: its padding is not read.
   const int n = a.new_lens ? a.new_lens[b] : a.T;
+  const bool turned = unit < ru;
+  const int c0 = turned ? unit : ru + unit, c1 = turned ? unit + ru : units + unit;
+  uint4 x[kAppendRows], y[kAppendRows];
+  const size_t tok = (size_t)b * a.T + min(t, a.T - 1);
+  auto fetch = [&](int row0) {
+#pragma unroll
+    for (int i = 0; i < kAppendRows; ++i) {
+      const int row = row0 + i * step;
+      if (t >= min(n, a.T) || row >= rows) continue;
+      const int kr = row - a.Hq, vr = kr - a.Hkv;
+      const uint16_t* src = kr < 0   ? a.q + tok * a.q_stride + (size_t)row * a.Hd
+                            : vr < 0 ? a.k + tok * a.k_stride + (size_t)kr * a.Hd
+                                     : a.v + tok * a.v_stride + (size_t)vr * a.Hd;
+      x[i] = reinterpret_cast<const uint4*>(src)[c0];
+      y[i] = reinterpret_cast<const uint4*>(src)[c1];
+    }
+  };
+  const int row_first = slot & (step - 1);
+  fetch(row_first);
+
+  const int pos = a.seq_lens[b];
   // The whole block of a sequence is refused together, so every CTA of the
   // sequence comes to the same answer before it writes.
   const bool len_ok = n >= 0 && n <= a.T;
@@ -108,44 +145,41 @@ __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArg
   ok = ok && !bad_page;
   const int there = ok ? n : 0;
 
-  const int units = a.Hd / 16, rows = a.Hq + 2 * a.Hkv, ru = a.rot / 16;
-  const int t0 = blockIdx.x * a.tokens, t1 = min(a.T, t0 + a.tokens);
-  const int mask = (1 << a.page_shift) - 1;
-  const int unit = tid % units, slot = tid / units, slots = kAppendCta / units;
-  const bool turned = unit < ru;
-  const int c0 = turned && !a.inter ? unit : 2 * unit, c1 = turned && !a.inter ? unit + ru : 2 * unit + 1;
-  for (int i = slot; i < (t1 - t0) * rows; i += slots) {
-    const int t = t0 + i / rows, row = i % rows;
-    const size_t tok = (size_t)b * a.T + t;
-    if (t >= there) {  // padding: nothing is cached, q_out is zero
-      if (row < a.Hq) {
-        uint4* dst = reinterpret_cast<uint4*>(a.q_out + (tok * a.Hq + row) * a.Hd);
-        dst[c0] = dst[c1] = make_uint4(0, 0, 0, 0);
-      }
-      continue;
-    }
+  if (t < a.T) {
+    const bool stored = t < there;
     const int l = pos + t;
-    const uint16_t* src;
-    uint16_t* out;
-    if (row < a.Hq) {
-      src = a.q + tok * a.q_stride + (size_t)row * a.Hd;
-      out = a.q_out + (tok * a.Hq + row) * a.Hd;
-    } else {
-      const int h = (row - a.Hq) % a.Hkv;
-      const bool is_v = row >= a.Hq + a.Hkv;
-      src = (is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) + (size_t)h * a.Hd;
-      const size_t at = ((((size_t)table[l >> a.page_shift] * a.Hkv + h) << a.page_shift) + (l & mask)) * a.Hd;
-      out = (is_v ? a.v_pages : a.k_pages) + at;
+    float4 c[2], s[2];
+    size_t page_row = 0;  // of head 0; a head further lies a page further
+    if (stored) {
+      page_row = (((size_t)table[l >> a.page_shift] * a.Hkv) << a.page_shift) + (l & ((1 << a.page_shift) - 1));
+      if (turned) {
+        const float4* cs = reinterpret_cast<const float4*>(a.cos_sin + (size_t)l * a.rot);
+        const float4* sn = cs + a.rot / 8;
+        const int i0 = a.inter ? unit : 2 * unit, i1 = a.inter ? unit + ru : 2 * unit + 1;
+        c[0] = cs[i0]; c[1] = cs[i1];
+        s[0] = sn[i0]; s[1] = sn[i1];
+      }
     }
-    uint4 x = reinterpret_cast<const uint4*>(src)[c0], y = reinterpret_cast<const uint4*>(src)[c1];
-    if (turned && row < a.Hq + a.Hkv) {
-      const float4* cs = reinterpret_cast<const float4*>(a.cos_sin + (size_t)l * a.rot) + 2 * unit;
-      const float4* sn = cs + a.rot / 8;
-      const float4 c[2] = {cs[0], cs[1]}, s[2] = {sn[0], sn[1]};
-      rotate_unit<BF16>(x, y, c, s, a.inter);
+    for (int row0 = row_first; row0 < rows; row0 += kAppendRows * step) {
+      if (row0 != row_first) fetch(row0);
+#pragma unroll
+      for (int i = 0; i < kAppendRows; ++i) {
+        const int row = row0 + i * step;
+        if (row >= rows) break;
+        const int kr = row - a.Hq, vr = kr - a.Hkv;
+        if (!stored) {  // padding: nothing is cached, q_out is zero
+          if (kr >= 0) break;
+          x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        } else if (turned && vr < 0) {
+          rotate_unit<BF16>(x[i], y[i], c, s, a.inter);
+        }
+        uint16_t* out = kr < 0   ? a.q_out + (tok * a.Hq + row) * a.Hd
+                        : vr < 0 ? a.k_pages + (page_row + ((size_t)kr << a.page_shift)) * a.Hd
+                                 : a.v_pages + (page_row + ((size_t)vr << a.page_shift)) * a.Hd;
+        reinterpret_cast<uint4*>(out)[c0] = x[i];
+        reinterpret_cast<uint4*>(out)[c1] = y[i];
+      }
     }
-    reinterpret_cast<uint4*>(out)[c0] = x;
-    reinterpret_cast<uint4*>(out)[c1] = y;
   }
 
   // The new length.  Written in place it must not be seen by a CTA of this
@@ -899,9 +933,14 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
   a.k_pages = static_cast<uint16_t*>(k_pages); a.v_pages = static_cast<uint16_t*>(v_pages);
   a.q_out = static_cast<uint16_t*>(q_out);
   a.counters = static_cast<int32_t*>(workspace); a.err = err;
-  // Enough CTAs to fill the SMs several times, at most 16 tokens in each.
-  a.tokens = (int)std::max<size_t>(1, std::min<size_t>(16, tok / (148 * 8)));
-  const dim3 grid((unsigned)std::max(1, (T + a.tokens - 1) / a.tokens), (unsigned)B);
+  // Threads enough on a token's rows that each has all of its own in flight at
+  // once; more of them when the tokens would not fill the SMs.
+  const int slots = kAppendCta / (Hd / 16);
+  a.row_slots = 1;
+  while (a.row_slots < slots && a.row_slots * kAppendRows < Hq + 2 * Hkv) a.row_slots *= 2;
+  while (a.row_slots < slots && tok * a.row_slots / slots < 148 * 4) a.row_slots *= 2;
+  const int tokens = slots / a.row_slots;
+  const dim3 grid((unsigned)std::max(1, (T + tokens - 1) / tokens), (unsigned)B);
   (void)cudaGetLastError();
   if (dtype == WSVD_DTYPE_BF16) kv_append_kernel<true><<<grid, kAppendCta, 0, as_stream(stream)>>>(a);
   else kv_append_kernel<false><<<grid, kAppendCta, 0, as_stream(stream)>>>(a);
