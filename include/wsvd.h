@@ -527,6 +527,34 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
                            const void* v_pages, int dtype, float softmax_scale, float* out, void* workspace,
                            size_t workspace_bytes, int32_t* err, void* stream);
 
+/* ---------------------------------------------------------------- paged latent cache
+ * The per-head latent cache of wsvd_decode_attention in pages (page_size,
+ * block_table and page ids as for the paged dense cache above):
+ *   lat_k, lat_v     [num_pages][H][page_size][r*bits/8] uint8,
+ *   scale_k, scale_v [num_pages][H][page_size] fp16,
+ * row by row the codes and scales of the contiguous cache.
+ *
+ * wsvd_decode_attention_paged: the operation, arguments and results of
+ * wsvd_decode_attention over the rows in the pages (one query per sequence and
+ * latent head, fp16 factors).  Both products over the rows are exact integer
+ * sums on the tensor cores: the codes against q' in 24-bit fixed point, and
+ * against the weights p_l * s_V,l in 22-bit fixed point relative to the largest
+ * of 32 to 128 rows.
+ *   workspace  as for wsvd_decode_attention (wsvd_decode_workspace_size(B, H, r)
+ *              bytes, ZERO before the first call); calls of the two may use one
+ *              in turn.
+ *   err        optional; WSVD_DEVERR_LEN_RANGE for seq_lens[b] < 0 or
+ *              > max_pages * page_size (that sequence's output is 0),
+ *              WSVD_DEVERR_PAGE_RANGE for a bad page (that sequence's output is
+ *              not valid).
+ * Rows >= seq_lens[b] are never used: their bytes may hold anything.  Two
+ * launches.                                                                 */
+int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits, int page_size, int num_pages, int max_pages,
+                                const int32_t* seq_lens, const int32_t* block_table, const void* q, int q_dtype,
+                                const uint8_t* lat_k, const uint8_t* lat_v, const void* scale_k, const void* scale_v,
+                                const void* B_k, const void* B_v, float softmax_scale, float* out, void* workspace,
+                                size_t workspace_bytes, int32_t* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

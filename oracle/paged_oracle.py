@@ -89,3 +89,55 @@ def decode_allowance(mass, wobble, Hd: int, n: int):
     and denominator, times sum p |v|."""
     d = (Hd / 16 + 4) * 2.0 ** -23 * wobble
     return 2 * mass * (2 * d[..., None] + 2.0 ** -20 + (n / 16 + 64) * 2.0 ** -23) + 1e-30
+
+
+def latent_codes(lat: np.ndarray, bits: int) -> np.ndarray:
+    """Integers of code bytes [..., r*bits/8] (4 bits: element 2j in the low half of byte j)."""
+    lat = np.asarray(lat, np.uint8)
+    if bits == 8:
+        return lat.view(np.int8).astype(np.float64)
+    both = np.stack([lat & 15, lat >> 4], axis=-1).astype(np.int64)
+    return np.where(both > 7, both - 16, both).reshape(lat.shape[:-1] + (-1,)).astype(np.float64)
+
+
+def latent_decode(q, lat_k, lat_v, scale_k, scale_v, B_k, B_v, table, lens, bits, scale=None):
+    """(out, mass, wobble) of the attention over paged latents: K and V rebuilt
+    row by row.  mass [B][H][Hd]: sum_l p_l sum_j |code_l,j s_l B_v[j, d]|; wobble
+    [B][H]: the largest sum_j |code_l,j s_l| max|q'| * scale, q' = B_k q."""
+    B, H, Hd = q.shape
+    scale = Hd ** -0.5 if scale is None else scale
+    out, mass, wobble = np.zeros(q.shape), np.zeros(q.shape), np.zeros((B, H))
+    ck, cv = latent_codes(lat_k, bits), latent_codes(lat_v, bits)
+    for b in range(B):
+        n = int(lens[b])
+        if not n:
+            continue
+        lk, lv = rows(ck, table, b, n), rows(cv, table, b, n)                      # [n][H][r]
+        sk = rows(np.asarray(scale_k, np.float64)[..., None], table, b, n)
+        sv = rows(np.asarray(scale_v, np.float64)[..., None], table, b, n)
+        for h in range(H):
+            K = (lk[:, h] * sk[:, h]) @ np.asarray(B_k[h], np.float64)
+            V = (lv[:, h] * sv[:, h]) @ np.asarray(B_v[h], np.float64)
+            qh = np.asarray(q[b, h], np.float64)
+            s = K @ qh * scale
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            out[b, h] = p @ V
+            mass[b, h] = p @ (np.abs(lv[:, h] * sv[:, h]) @ np.abs(np.asarray(B_v[h], np.float64)))
+            qp = np.abs(np.asarray(B_k[h], np.float64)) @ np.abs(qh)
+            wobble[b, h] = np.abs(lk[:, h] * sk[:, h]).sum(1).max() * qp.max() * abs(scale)
+    return out, mass, wobble
+
+
+def latent_allowance(mass, wobble, r: int, Hd: int, biggest: np.ndarray, n: int):
+    """How far an fp32 / fixed-point computation of `latent_decode` may be off.
+    q' is an fp32 sum of Hd products (at most (Hd / 32 + 8) 2^-24 of its
+    magnitudes) in fixed point to half of 2^-22 of its largest value; a logit is
+    an exact integer sum scaled in fp32 (4 roundings): off by
+    d <= (Hd / 32 + 16) 2^-23 wobble.  A weight is off by 2 d and 2^-21, and is
+    cut to half a step of 2^-21 of the largest weight of its strip, which with
+    its codes makes at most 2^-21 * biggest a row, biggest[b, h, d] the largest
+    |V| a full code row can give, over the joined mass of all weights: no more
+    than `biggest` times 2^-21 a row.  Sums as in decode_allowance, then r more."""
+    d = (Hd / 32 + 16) * 2.0 ** -23 * wobble
+    return 2 * mass * (2 * d[..., None] + 2.0 ** -20 + (n / 16 + 64 + r) * 2.0 ** -23) + biggest * 2.0 ** -21 + 1e-30

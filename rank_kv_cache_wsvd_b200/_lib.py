@@ -68,6 +68,8 @@ SIGNATURES = {
     "paged_kv_append": (_c_int, [_c_int] * 11 + [_p, _c_ll] * 3 + [_c_int] + [_p] * 9 + [_c_size, _p, _p]),
     "paged_decode_workspace_size": (_c_size, [_c_int] * 5),
     "paged_decode_attention": (_c_int, [_c_int] * 8 + [_p] * 5 + [_c_int, _c_float, _p, _p, _c_size, _p, _p]),
+    "wsvd_decode_attention_paged": (_c_int, [_c_int] * 8 + [_p] * 3 + [_c_int] + [_p] * 6 + [_c_float, _p, _p, _c_size,
+                                                                                              _p, _p]),
     "shared_latent_svd_decode": (_c_int, [_c_int] * 5 + [_p, _p, _c_int] + [_p] * 4 + [_c_float, _p, _p, _c_size,
                                                                                          _p, _p]),
 }
@@ -452,6 +454,36 @@ def paged_decode_attention(q, k_pages, v_pages, block_table, seq_lens, softmax_s
                  None if err is None else _dense(err, torch.int32, err.shape, dev, "err"), _raw_stream(stream, dev))
     if st:
         _check(st, "paged_decode_attention")
+    return out
+
+
+# ----------------------------------------------------------------------------- paged latent cache
+def wsvd_decode_attention_paged(q, lat_k, lat_v, scale_k, scale_v, B_k, B_v, block_table, seq_lens, bits: int,
+                                softmax_scale: float = 0.0, out=None, workspace_buf=None, err=None, stream=None):
+    """wsvd_decode_attention over latents in pages: lat_k, lat_v
+    [num_pages][H][page_size][r*bits/8], scale_k, scale_v [num_pages][H][page_size],
+    block_table [B][max_pages].  Returns out [B][H][Hd] fp32."""
+    lib = load()
+    B, H, Hd = shape = q.shape
+    num_pages, _, page_size, rb = lat_k.shape
+    max_pages = block_table.shape[1]
+    r, dev, f16, u8 = rb * 8 // bits, q.get_device(), torch.float16, torch.uint8
+    code = _dtype_code(q)
+    if out is None:
+        out = _new(torch.empty, shape, torch.float32, dev, stream)
+    codes, scales, ups = (num_pages, H, page_size, rb), (num_pages, H, page_size), (H, r, Hd)
+    ws = _scratch(workspace_buf, dev, stream, lib.wsvd_decode_workspace_size, B, H, r)
+    st = _launch(dev, lib.wsvd_decode_attention_paged, B, H, Hd, r, bits, page_size, num_pages, max_pages,
+                 _dense(seq_lens, torch.int32, (B,), dev, "seq_lens"),
+                 _dense(block_table, torch.int32, (B, max_pages), dev, "block_table"),
+                 _dense(q, q.dtype, shape, dev, "q"), code, _dense(lat_k, u8, codes, dev, "lat_k"),
+                 _dense(lat_v, u8, codes, dev, "lat_v"), _dense(scale_k, f16, scales, dev, "scale_k"),
+                 _dense(scale_v, f16, scales, dev, "scale_v"), _dense(B_k, f16, ups, dev, "B_k"),
+                 _dense(B_v, f16, ups, dev, "B_v"), softmax_scale, _dense(out, torch.float32, shape, dev, "out"),
+                 ws.data_ptr(), ws.numel(), None if err is None else _dense(err, torch.int32, err.shape, dev, "err"),
+                 _raw_stream(stream, dev))
+    if st:
+        _check(st, "wsvd_decode_attention_paged")
     return out
 
 

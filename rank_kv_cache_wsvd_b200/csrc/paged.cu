@@ -12,6 +12,7 @@
 #include <tuple>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 using namespace wsvd;
 
@@ -243,8 +244,8 @@ struct DecCfg {
 __host__ __device__ constexpr int partial_floats(int queries, int Hd) { return queries * Hd + (2 * queries + 3) / 4 * 4; }
 
 struct KvDecodeArgs {
-  int B, Tq, Hq, Hkv, G, nq, chunks, page_shift, num_pages, max_pages, cap, ctas;
-  const int32_t* seq_lens;
+  PagedSeqs seqs;  // a unit: a KV head and a chunk of its queries
+  int Tq, Hq, Hkv, G, nq, chunks, page_shift, num_pages, max_pages, ctas;
   const int32_t* block_table;
   const uint16_t *q, *k, *v;
   float* out;
@@ -254,26 +255,6 @@ struct KvDecodeArgs {
   float qscale;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ uint32_t movm_t(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -303,47 +284,10 @@ __device__ __forceinline__ uint32_t strip_off(int r, int c) {
   return (uint32_t)(r * HD * 2 + ((c ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ int valid_len(const KvDecodeArgs& a, int b) {
-  const int n = a.seq_lens[b];
-  return n < 0 || n > a.cap ? 0 : n;
-}
-
-// What a segment costs beside its strips (queries, joins), in strips.  A unit
-// counts as its strips plus so many when the CTAs' shares are cut, else a CTA
-// that meets many short sequences would be the last to finish.
+// Strips that a segment's fixed cost counts as.  Measured (a ragged batch with
+// four tokens a sequence, 0 / 8 / 16 / 24 strips): 33.9 / 26.3 / 25.6 / 25.9 us; 32
+// heads of 1600 rows 12.4 / 11.7 / 10.6 / 10.6 us.
 constexpr int kLead = 24;
-
-template <int TS>
-__device__ __forceinline__ int counted(int n) {  // a unit of a sequence with n rows
-  return n > 0 ? (n + TS - 1) / TS + kLead : 0;
-}
-
-// A segment: strips [s, e) of unit u (KV head * chunks + chunk) of sequence b;
-// none when the CTA's share of the unit ends within the lead.
-template <int TS>
-struct Segment {
-  int b, u, n, s, e;
-  int at, taken;   // where the CTA's share begins in the unit (lead included), and how much of the unit it takes
-  long long left;  // of the CTA's share from here on
-  __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
-  __device__ __forceinline__ void enter(int place) {
-    at = place;
-    taken = (int)min((long long)(strips() + kLead - at), left);
-    s = max(0, at - kLead);
-    e = max(0, at + taken - kLead);
-  }
-  __device__ __forceinline__ bool next(const KvDecodeArgs& a) {
-    left -= taken;
-    if (left <= 0) return false;
-    if (++u == a.Hkv * a.chunks) {
-      u = 0;
-      do n = valid_len(a, ++b);
-      while (n == 0);
-    }
-    enter(0);
-    return true;
-  }
-};
 
 template <bool BF16, int HD, int NB>
 __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_kernel(const KvDecodeArgs a) {
@@ -356,71 +300,27 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   __shared__ int sm_valid[NW][S];
   __shared__ int sm_slot[NW], sm_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
-  const int c = blockIdx.x, units = a.Hkv * a.chunks;
+  const int c = blockIdx.x;
+  const PagedSeqs& seqs = a.seqs;
 
-  // The strips of all sequences, and where this CTA's share starts: every warp
-  // finds it for itself.
-  const int per = (a.B + 31) / 32;
-  const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
-  long long sum = 0;
-#pragma unroll 4
-  for (int b = b0; b < b1; ++b) {
-    const int raw = a.seq_lens[b];
-    if ((raw < 0 || raw > a.cap) && c == 0) set_err(a.err, WSVD_DEVERR_LEN_RANGE);
-    sum += counted<TS>(valid_len(a, b));
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const long long total = __shfl_sync(0xffffffffu, incl, 31), before = incl - sum;
-  const long long G = total * units;
   // Sequences without rows: zeros, spread over the CTAs.
-  for (int b = c; b < a.B; b += gridDim.x)
-    if (valid_len(a, b) == 0)
+  for (int b = c; b < seqs.B; b += gridDim.x)
+    if (seqs.rows(b) == 0)
       for (int i = tid; i < a.Tq * a.Hq * HD; i += C::kThreads) a.out[(size_t)b * a.Tq * a.Hq * HD + i] = 0.f;
-  // At least one strip per warp, so that a small problem is not cut too finely.
-  const long long most = (G + NW - 1) / NW;
-  const int CW = (int)(most < a.ctas ? most : a.ctas);
-  if (c >= CW) return;
-  // The first `extra` CTAs take one strip more than the others.
-  const unsigned long long uG = (unsigned long long)G;
-  const long long base = uG < 0x80000000ull ? (uint32_t)G / (uint32_t)CW : G / CW, extra = G - base * CW;
-  const long long g_begin = base * c + min((long long)c, extra), g_end = g_begin + base + (c < extra ? 1 : 0);
-  auto cta_of = [&](long long strip) {  // whose share holds a strip
-    const long long big = extra * (base + 1);
-    return (int)(strip < big ? strip / (base + 1) : extra + (strip - big) / base);
-  };
-  const bool mine = g_begin >= before * units && g_begin < (before + sum) * units;
-  long long rem = g_begin - before * units;
-  int sb = b0;
-  if (mine)
-    for (;; ++sb) {
-      const long long ns = (long long)counted<TS>(valid_len(a, sb)) * units;
-      if (rem < ns) break;
-      rem -= ns;
-    }
-  const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-  Segment<TS> seg;
-  seg.b = __shfl_sync(0xffffffffu, sb, src);
-  rem = __shfl_sync(0xffffffffu, rem, src);
-  seg.n = valid_len(a, seg.b);
-  seg.u = (int)(rem / (seg.strips() + kLead));
-  seg.left = g_end - g_begin;
-  seg.enter((int)(rem % (seg.strips() + kLead)));
+  Strips<TS, kLead> share;
+  typename Strips<TS, kLead>::Segment seg;
+  if (!share.deal(seqs, a.ctas, NW, a.err, &seg)) return;
 
   // ---- the warp's copies: cursor `ld`, page ids one strip ahead
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
-  Segment<TS> ld = seg;
+  auto ld = seg;
   int ls = ld.s + warp;
   bool more = true;
   int pg[MT];
   const int page_mask = (1 << a.page_shift) - 1;
   auto settle = [&]() {  // the next strip of this warp, and its pages
     while (more && ls >= ld.e) {
-      more = ld.next(a);
+      more = ld.next(seqs);
       ls = ld.s + warp;
     }
     if (more) {
@@ -466,7 +366,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   int stage = 0;  // of the next strip to read
 
   // ---- segment by segment
-  for (bool go = true; go; go = seg.next(a)) {
+  for (bool go = true; go; go = seg.next(seqs)) {
     if (seg.s == seg.e) continue;
     const int h = seg.u / a.chunks, j0 = (seg.u % a.chunks) * C::kQ;
     const int nq = min(C::kQ, a.nq - j0);
@@ -737,10 +637,9 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     // ---- a unit cut over several CTAs: the last to arrive joins the partials
     // in the order of the CTAs, so the result does not depend on who that is.
     if (!whole) {
-      // the place of the unit's first strip in the whole order
-      const long long u0 = g_end - seg.left - seg.at + kLead;
-      const int cf = cta_of(u0), np = cta_of(u0 + ns - 1) - cf + 1;
-      const size_t unit = (size_t)seg.b * units + seg.u;
+      int cf, np;
+      share.holders(seg, &cf, &np);
+      const size_t unit = (size_t)seg.b * seqs.units + seg.u;
       __threadfence();
       __syncthreads();
       if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + unit, 1) == np - 1;
@@ -794,15 +693,6 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-// Whether [p, p + np) and [q, q + nq) share a byte.
-inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return np && nq && a < b + nq && b < a + np;
-}
-
-// Upper bound of the decode's grid; sizes its partials.
-constexpr int kMaxPagedCtas = 592;
-
 // Queries per chunk: two column blocks of 8, one at head size 256 (registers).
 inline int chunk_queries(int nq, int Hd) { return nq > 8 && Hd != 256 ? 16 : 8; }
 
@@ -827,36 +717,6 @@ DecodeKernel pick_decode(int Hd, int qc) {
   }
 }
 
-// SM count and resident CTAs of a kernel on the current device (the shared
-// memory opt-in is made on the way), asked once per device and kernel.
-cudaError_t resident_ctas(const DecodeKernel& k, int* ctas) {
-  static std::mutex mu;
-  static std::map<std::pair<int, const void*>, int> known;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(dev, reinterpret_cast<const void*>(k.fn));
-  auto it = known.find(key);
-  if (it == known.end()) {
-    int sms = 0, occ = 0;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(key.second, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
-    if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, k.threads, k.smem);
-    if (e != cudaSuccess) return e;
-    it = known.emplace(key, std::min(kMaxPagedCtas, sms * std::max(1, occ))).first;
-  }
-  *ctas = it->second;
-  return cudaSuccess;
-}
-
-int page_shift_of(int page_size) {
-  for (int s = 4; s <= 8; ++s)
-    if (page_size == 1 << s) return s;
-  return -1;
-}
-
 struct DecodeWs {
   size_t partials, counters, total;
 };
@@ -870,6 +730,27 @@ DecodeWs decode_ws(int B, int Tq, int Hq, int Hkv, int Hd) {
 }
 
 }  // namespace
+
+cudaError_t wsvd::paged_resident_ctas(const void* fn, int threads, size_t smem, int* ctas) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(dev, fn);
+  auto it = known.find(key);
+  if (it == known.end()) {
+    int sms = 0, occ = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem)) != cudaSuccess)
+      return e;
+    it = known.emplace(key, std::min(kMaxPagedCtas, sms * std::max(1, occ))).first;
+  }
+  *ctas = it->second;
+  return cudaSuccess;
+}
 
 extern "C" {
 
@@ -972,9 +853,9 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   const int qc = chunk_queries((int)nq, Hd);
   const DecodeKernel kern = dtype == WSVD_DTYPE_BF16 ? pick_decode<true>(Hd, qc) : pick_decode<false>(Hd, qc);
   KvDecodeArgs a{};
-  a.B = B; a.Tq = Tq; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.nq = (int)nq; a.chunks = (int)((nq + qc - 1) / qc);
-  a.page_shift = shift; a.num_pages = num_pages; a.max_pages = max_pages; a.cap = max_pages << shift;
-  a.seq_lens = seq_lens; a.block_table = block_table;
+  a.Tq = Tq; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.nq = (int)nq; a.chunks = (int)((nq + qc - 1) / qc);
+  a.seqs = PagedSeqs{B, Hkv * a.chunks, max_pages << shift, seq_lens};
+  a.page_shift = shift; a.num_pages = num_pages; a.max_pages = max_pages; a.block_table = block_table;
   a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k_pages);
   a.v = static_cast<const uint16_t*>(v_pages);
   a.out = out;
@@ -983,7 +864,7 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   a.err = err;
   a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
   (void)cudaGetLastError();
-  if (resident_ctas(kern, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
+  if (paged_resident_ctas(reinterpret_cast<const void*>(kern.fn), kern.threads, kern.smem, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
   kern.fn<<<a.ctas, kern.threads, kern.smem, as_stream(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
 }

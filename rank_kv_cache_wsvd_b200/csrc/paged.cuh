@@ -1,0 +1,164 @@
+// Shared by the paged kernels: how the strips of ragged sequences are dealt to
+// CTAs, the warp's copies, and host helpers of the entry points.
+#pragma once
+
+#include "common.cuh"
+
+namespace wsvd {
+
+// ------------------------------------------------------------------ dealing strips to CTAs
+// The sequences of a call and their units: every sequence has `units` of them
+// (a head, or a head and a group of queries), each over all of its rows.
+struct PagedSeqs {
+  int B, units, cap;  // cap: rows the page table has room for
+  const int32_t* seq_lens;
+  __device__ __forceinline__ int rows(int b) const {  // a length out of range counts as none
+    const int n = seq_lens[b];
+    return n < 0 || n > cap ? 0 : n;
+  }
+};
+
+// A unit's rows are cut into strips of TS rows, and counts as its strips plus
+// LEAD (what a segment costs beside its strips: queries, joins) when the CTAs'
+// shares are cut, else a CTA that meets many short sequences would finish last.
+template <int TS, int LEAD>
+struct Strips {
+  // The CTA's share of one unit: strips [s, e) of unit u of sequence b (n
+  // rows); none when the share ends within the lead.
+  struct Segment {
+    int b, u, n, s, e;
+    int at, taken;   // where the share begins in the unit (lead included), and how much of the unit it takes
+    long long left;  // of the CTA's share from here on
+    __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
+    __device__ __forceinline__ void enter(int place) {
+      at = place;
+      taken = (int)min((long long)(strips() + LEAD - at), left);
+      s = max(0, at - LEAD);
+      e = max(0, at + taken - LEAD);
+    }
+    __device__ __forceinline__ bool next(const PagedSeqs& q) {
+      left -= taken;
+      if (left <= 0) return false;
+      if (++u == q.units) {
+        u = 0;
+        do n = q.rows(++b);
+        while (n == 0);
+      }
+      enter(0);
+      return true;
+    }
+  };
+
+  static __device__ __forceinline__ int counted(int n) { return n > 0 ? (n + TS - 1) / TS + LEAD : 0; }
+
+  long long total, base, extra, end;  // strips in all; per CTA; CTAs with one more; this CTA's end
+  int ctas;                           // CTAs that have a share
+
+  __device__ __forceinline__ long long begin_of(int c) const { return base * c + min((long long)c, extra); }
+  __device__ __forceinline__ int cta_of(long long strip) const {  // whose share holds a strip
+    const long long big = extra * (base + 1);
+    return (int)(strip < big ? strip / (base + 1) : extra + (strip - big) / base);
+  }
+  // The CTAs that hold strips of the segment's unit: the first, and how many.
+  __device__ __forceinline__ void holders(const Segment& g, int* first, int* count) const {
+    const long long u0 = end - g.left - g.at + LEAD;  // the unit's first strip in the whole order
+    *first = cta_of(u0);
+    *count = cta_of(u0 + g.strips() - 1) - *first + 1;
+  }
+
+  // This CTA's share and its first segment; false when it has none.  Every warp
+  // finds it for itself (all lanes take part).  `least`: strips a CTA takes at
+  // least, so that a small problem is not cut too finely.
+  __device__ __forceinline__ bool deal(const PagedSeqs& q, int grid, int least, int32_t* err, Segment* seg) {
+    const int lane = threadIdx.x & 31, c = blockIdx.x;
+    const int per = (q.B + 31) / 32;
+    const int b0 = min(q.B, lane * per), b1 = min(q.B, b0 + per);
+    long long sum = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
+      const int raw = q.seq_lens[b];
+      if ((raw < 0 || raw > q.cap) && c == 0) set_err(err, WSVD_DEVERR_LEN_RANGE);
+      sum += counted(q.rows(b));
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const long long before = (incl - sum) * q.units;
+    total = __shfl_sync(0xffffffffu, incl, 31) * q.units;
+    const long long most = (total + least - 1) / least;
+    ctas = (int)(most < grid ? most : grid);
+    if (c >= ctas) return false;
+    base = (unsigned long long)total < 0x80000000ull ? (uint32_t)total / (uint32_t)ctas : total / ctas;
+    extra = total - base * ctas;
+    const long long begin = begin_of(c);
+    end = begin + base + (c < extra ? 1 : 0);
+    const bool mine = begin >= before && begin < before + sum * q.units;
+    long long rem = begin - before;
+    int sb = b0;
+    if (mine)
+      for (;; ++sb) {
+        const long long ns = (long long)counted(q.rows(sb)) * q.units;
+        if (rem < ns) break;
+        rem -= ns;
+      }
+    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    seg->b = __shfl_sync(0xffffffffu, sb, src);
+    rem = __shfl_sync(0xffffffffu, rem, src);
+    seg->n = q.rows(seg->b);
+    seg->left = end - begin;
+    const int unit = seg->strips() + LEAD;
+    seg->u = (int)(rem / unit);
+    seg->enter((int)(rem % unit));
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ warp copies and fragments
+// 16 bytes to shared memory; `bytes` 0 reads nothing and fills with zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// ------------------------------------------------------------------ host
+// Upper bound of the paged decodes' grids; sizes their partial results.
+constexpr int kMaxPagedCtas = 592;
+
+// log2 of a page size the paged caches take (16 .. 256), else -1.
+inline int page_shift_of(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+// Whether [p, p + np) and [q, q + nq) share a byte.
+inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return np && nq && a < b + nq && b < a + np;
+}
+
+// CTAs of a kernel that the current device holds at once, at most
+// kMaxPagedCtas (its shared-memory opt-in is made on the way); asked once per
+// device and kernel.
+cudaError_t paged_resident_ctas(const void* fn, int threads, size_t smem, int* ctas);
+
+}  // namespace wsvd

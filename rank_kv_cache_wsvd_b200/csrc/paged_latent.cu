@@ -1,0 +1,573 @@
+// Decode attention over per-head low-rank latents (int8 / int4 codes with an
+// fp16 scale per row) that lie in pages, for sm_100a: the operation of
+// wsvd_decode_attention, reassociated the same way
+//   q' = B_Kh . q,  s_l = s^K_l (code^K_l . q') * softmax_scale,
+//   o = sum_l p_l s^V_l code^V_l,  out = (o / sum_l p_l) . B_Vh,
+// with both products over the rows as integer matrix instructions on the codes
+// as they are stored:
+//   scores  m16n8k32: 16 rows x 32 codes against q' as a fixed-point number in
+//           three signed base-256 digits (24 bits), a digit per column;
+//   values  m16n8k32: 16 latent columns x 32 rows (ldmatrix transposes the
+//           bytes) against w_l = p_l s^V_l, cut into three digits the same way
+//           relative to the strip's largest weight (22 bits).
+// Both sums are exact; int4 codes enter as 16 times their value, so that one
+// mask or shift unpacks them.  Against one dp4a chain and one conversion per
+// code (the contiguous decode) this takes most of the per-row work off the
+// issue slots, which bound that kernel for short rows.
+//
+// Work is dealt as in the dense paged decode: strips of rows over a grid of
+// CTAs, every warp its own cp.async pipeline, partial results of a head that
+// several CTAs share joined by the last of them.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "paged.cuh"
+#include "wsvd_internal.h"
+
+using namespace wsvd;
+
+namespace {
+
+constexpr int kDigitMax = 127 * 65536 + 127 * 256 + 127;  // largest number of three signed digits
+constexpr int kDigitBias = 0x808080;  // x + bias holds the digits + 128, a byte each
+
+// BITS per code, RB bytes per row.
+template <int BITS, int RB>
+struct LatCfg {
+  static constexpr int kR = RB * 8 / BITS;                // codes per row
+  static constexpr int kTS = RB <= 32 ? 128 : (RB == 64 ? 64 : 32);  // rows per strip
+  static constexpr int kBlocks = kTS / 32;                // of 32 rows, one per lane
+  static constexpr int kGroups = kTS / 16;                // of 16 rows, within one page each
+  static constexpr int kHalf = kTS * RB;
+  static constexpr int kStage = 2 * kHalf + 2 * kTS * 2;  // K codes, V codes, K scales, V scales
+#ifndef LT_WARPS
+#define LT_WARPS (RB == 16 ? 16 : 12)
+#endif
+#ifndef LT_STAGES
+#define LT_STAGES 2
+#endif
+#ifndef LT_LEAD
+#define LT_LEAD 24
+#endif
+  static constexpr int kWarps = LT_WARPS, kStages = LT_STAGES, kLead = LT_LEAD;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kKS = kR >= 32 ? kR / 32 : 1;      // k steps of the score product
+  static constexpr int kChunks = RB / 16;                 // 16-byte chunks of a row
+  static constexpr int kDG = kR / 16;                     // groups of 16 latent columns
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+};
+
+struct LatDecodeArgs {
+  PagedSeqs seqs;  // a unit: a head
+  int H, Hd, page_shift, num_pages, max_pages, ctas;
+  const int32_t* block_table;
+  const uint8_t *lat_k, *lat_v;
+  const __half *scale_k, *scale_v;
+  const float* qglobal;  // [B][H][r]
+  const __half* Bv;      // [H][r][Hd]
+  float* out;
+  float* partials;       // [2 * ctas][r + 4]: o, then m, l
+  int32_t* counters;
+  int32_t* err;
+  float qscale;
+};
+
+__device__ __forceinline__ void imma32(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void imma16(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k16.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+// Two transposed 16 x 16 byte blocks: lanes 0-15 give the rows of the first,
+// 16-31 of the second; the registers are the row operand of m16n8k32 for the
+// blocks' columns (16) x rows (32).
+__device__ __forceinline__ void ldsm_bytes_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ int warp_max_s32(int v) {
+  int r;
+  asm volatile("redux.sync.max.s32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Order of floats as integers, and back (NaN above infinity).
+__device__ __forceinline__ int float_key(float x) {
+  const int b = __float_as_int(x);
+  return b >= 0 ? b : b ^ 0x7fffffff;
+}
+__device__ __forceinline__ float key_float(int k) { return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff); }
+
+// Offset of 16-byte chunk c of row r: rows that share a bank column at one
+// chunk index are turned apart.
+template <int RB>
+__device__ __forceinline__ uint32_t lat_off(int r, int c) {
+  constexpr int kTurn = RB == 16 ? 0 : (RB == 32 ? 2 : (RB == 64 ? 1 : 0));
+  return (uint32_t)(r * RB + ((c ^ ((r >> kTurn) & (RB / 16 - 1))) << 4));
+}
+
+// Four bytes, byte `k` of each of four words.
+__device__ __forceinline__ uint32_t bytes_of(const uint4& w, uint32_t sel) {
+  return __byte_perm(__byte_perm(w.x, w.y, sel), __byte_perm(w.z, w.w, sel), 0x5410);
+}
+
+template <int BITS, int RB>
+__global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kernel(const LatDecodeArgs a) {
+  using C = LatCfg<BITS, RB>;
+  constexpr int TS = C::kTS, S = C::kStages, NW = C::kWarps, R = C::kR, KS = C::kKS, NBL = C::kBlocks, DG = C::kDG;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float sm_o[NW][R], sm_m[NW], sm_l[NW];
+  __shared__ __align__(16) uint32_t sm_w[NW][TS];
+  __shared__ float sm_res[R + 1], sm_up[C::kThreads * 2];
+  __shared__ int sm_valid[NW][S], sm_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
+  const int c = blockIdx.x, H = a.H, Hd = a.Hd;
+  const PagedSeqs& seqs = a.seqs;
+
+  for (int b = c; b < seqs.B; b += gridDim.x)
+    if (seqs.rows(b) == 0)
+      for (int i = tid; i < H * Hd; i += C::kThreads) a.out[(size_t)b * H * Hd + i] = 0.f;
+  Strips<TS, C::kLead> share;
+  typename Strips<TS, C::kLead>::Segment seg;
+  if (!share.deal(seqs, a.ctas, NW, a.err, &seg)) {
+    griddep_wait();  // the grid never completes before the q' grid it was launched behind
+    return;
+  }
+
+  // ---- the warp's copies: cursor `ld`; lane i holds the page of 16-row group i
+  const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
+  auto ld = seg;
+  int ls = ld.s + warp;
+  bool more = true;
+  int pg = -1;
+  const int page_mask = (1 << a.page_shift) - 1;
+  auto settle = [&]() {  // the next strip of this warp, and its pages
+    while (more && ls >= ld.e) {
+      more = ld.next(seqs);
+      ls = ld.s + warp;
+    }
+    if (more) {
+      const int l = ls * TS + lane * 16;
+      pg = lane < C::kGroups && l < ld.n ? __ldg(a.block_table + (size_t)ld.b * a.max_pages + (l >> a.page_shift)) : -1;
+    }
+  };
+  auto issue = [&](int stage) {
+    if (more) {
+      const uint32_t dst = my_ring + (uint32_t)stage * C::kStage;
+      const int l0 = ls * TS;
+      const bool in = pg >= 0 && pg < a.num_pages;
+      if (lane < C::kGroups && !in && l0 + lane * 16 < ld.n) set_err(a.err, WSVD_DEVERR_PAGE_RANGE);
+      const int valid = (int)(__ballot_sync(0xffffffffu, in) & ((1u << C::kGroups) - 1));
+      // Codes: whole groups of 16 rows (rows past the length lie in the same
+      // page; they are masked later).
+      constexpr int kRowsPer = 512 / RB;  // rows of one copy instruction
+#pragma unroll
+      for (int j = 0; j < TS / kRowsPer; ++j) {
+        const int r = j * kRowsPer + lane / C::kChunks, ch = lane % C::kChunks, grp = r / 16;
+        const int p = __shfl_sync(0xffffffffu, pg, grp);
+        const bool there = (valid >> grp) & 1;
+        const size_t row = (((size_t)(there ? p : 0) * H + ld.u) << a.page_shift) + ((l0 + r) & page_mask);
+        const size_t src = there ? row * RB + ch * 16 : 0;
+        const uint32_t off = lat_off<RB>(r, ch);
+        cp_async16(dst + off, a.lat_k + src, there ? 16u : 0u);
+        cp_async16(dst + C::kHalf + off, a.lat_v + src, there ? 16u : 0u);
+      }
+      {  // scales: 8 rows a copy, K then V
+        constexpr int kPer = TS / 8;
+        const int i = lane % kPer, grp = i / 2;
+        const int p = __shfl_sync(0xffffffffu, pg, grp);
+        if (lane < 2 * kPer) {
+          const bool there = (valid >> grp) & 1;
+          const size_t row = (((size_t)(there ? p : 0) * H + ld.u) << a.page_shift) + ((l0 + i * 8) & page_mask);
+          cp_async16(dst + 2 * C::kHalf + lane * 16, (lane < kPer ? a.scale_k : a.scale_v) + (there ? row : 0),
+                     there ? 16u : 0u);
+        }
+      }
+      if (lane == 0) sm_valid[warp][stage] = valid;
+      ls += NW;
+      settle();
+    }
+    cp_commit();
+  };
+  settle();
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  int stage = 0;
+  griddep_wait();  // q'
+
+  // A lane's row within a block of 32, in the score product's order of rows.
+  const int tok = ((c4 >> 1) << 4) | ((c4 & 1) << 3) | g;
+  // Weight digits: column g takes byte 2 - g (the high digit first); columns
+  // from 3 on are zero.
+  const uint32_t wsel = g < 3 ? (uint32_t)((2 - g) | ((6 - g) << 4)) : 0u, wmask = g < 3 ? 0xffffffffu : 0u;
+
+  for (bool go = true; go; go = seg.next(seqs)) {
+    if (seg.s == seg.e) continue;
+    const int h = seg.u;
+    const size_t bh = (size_t)seg.b * H + h;
+
+    // ---- q' as signed digits in the score product's column operand: even
+    // columns the high digit, odd ones the middle; a second operand the low.
+    uint32_t qhm[KS][2], qlo[KS][2];
+    float qstep;
+    {
+      const float* qg = a.qglobal + bh * R;
+      float amax = 0.f;
+      for (int j = lane; j < R; j += 32) amax = fmaxf(amax, fabsf(__ldcg(qg + j)));
+      amax = key_float(warp_max_s32(float_key(amax)));
+      const float inv = amax > 0.f ? (float)kDigitMax / amax : 0.f;
+      qstep = amax / (float)kDigitMax * a.qscale * (BITS == 4 ? 0.0625f : 1.f);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t hm = 0, lo = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = BITS == 8 ? k * 32 + x * 16 + 4 * c4 + i : k * 32 + 8 * c4 + 2 * i + x;
+            int v = 0;
+            if (R >= 32 || x == 0) v = max(-kDigitMax, min(kDigitMax, __float2int_rn(__ldcg(qg + e) * inv)));
+            const uint32_t y = (uint32_t)(v + kDigitBias);
+            hm |= ((y >> (g & 1 ? 8 : 16)) & 0xffu) << (8 * i);
+            lo |= (y & 0xffu) << (8 * i);
+          }
+          qhm[k][x] = hm ^ 0x80808080u;
+          qlo[k][x] = lo ^ 0x80808080u;
+        }
+    }
+
+    float m = kNegInf, l = 0.f, o[DG][4];
+#pragma unroll
+    for (int d = 0; d < DG; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+
+    for (int s = seg.s + warp; s < seg.e; s += NW) {
+      cp_wait<S - 2>();
+      __syncwarp();
+      issue(stage == 0 ? S - 1 : stage - 1);
+      const uint32_t kb = my_ring + (uint32_t)stage * C::kStage, vb = kb + C::kHalf, sb = vb + C::kHalf;
+      const int valid = sm_valid[warp][stage];
+      const bool masked = s * TS + TS > seg.n || valid != (1 << C::kGroups) - 1;
+
+      // ---- scores: lane `lane` ends with row tok of every block
+      float sc[NBL];
+#pragma unroll
+      for (int blk = 0; blk < NBL; ++blk) {
+        int hm[2][4] = {}, lo[2][4] = {};
+        if constexpr (RB == 16) {  // 32 rows of one chunk in one load
+          uint32_t f[4];
+          ldsm4(f, kb + lat_off<RB>(blk * 32 + lane, 0));
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if constexpr (BITS == 8) {
+              imma16(hm[t], f[2 * t], f[2 * t + 1], qhm[0][0]);
+              imma16(lo[t], f[2 * t], f[2 * t + 1], qlo[0][0]);
+            } else {
+              const uint32_t e0 = (f[2 * t] << 4) & 0xf0f0f0f0u, e1 = (f[2 * t + 1] << 4) & 0xf0f0f0f0u;
+              const uint32_t d0 = f[2 * t] & 0xf0f0f0f0u, d1 = f[2 * t + 1] & 0xf0f0f0f0u;
+              imma32(hm[t], e0, e1, d0, d1, qhm[0][0], qhm[0][1]);
+              imma32(lo[t], e0, e1, d0, d1, qlo[0][0], qlo[0][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int cp = 0; cp < C::kChunks / 2; ++cp)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              uint32_t f[4];
+              ldsm4(f, kb + lat_off<RB>(blk * 32 + t * 16 + (lane & 15), 2 * cp + (lane >> 4)));
+              if constexpr (BITS == 8) {
+                imma32(hm[t], f[0], f[1], f[2], f[3], qhm[cp][0], qhm[cp][1]);
+                imma32(lo[t], f[0], f[1], f[2], f[3], qlo[cp][0], qlo[cp][1]);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t e0 = (f[2 * x] << 4) & 0xf0f0f0f0u, e1 = (f[2 * x + 1] << 4) & 0xf0f0f0f0u;
+                  const uint32_t d0 = f[2 * x] & 0xf0f0f0f0u, d1 = f[2 * x + 1] & 0xf0f0f0f0u;
+                  imma32(hm[t], e0, e1, d0, d1, qhm[2 * cp + x][0], qhm[2 * cp + x][1]);
+                  imma32(lo[t], e0, e1, d0, d1, qlo[2 * cp + x][0], qlo[2 * cp + x][1]);
+                }
+              }
+            }
+        }
+        const bool t1 = c4 & 2, r1 = c4 & 1;
+        const int ih = t1 ? (r1 ? hm[1][2] : hm[1][0]) : (r1 ? hm[0][2] : hm[0][0]);
+        const int im = t1 ? (r1 ? hm[1][3] : hm[1][1]) : (r1 ? hm[0][3] : hm[0][1]);
+        const int il = t1 ? (r1 ? lo[1][2] : lo[1][0]) : (r1 ? lo[0][2] : lo[0][0]);
+        const float dot = fmaf((float)ih, 65536.f, fmaf((float)im, 256.f, (float)il));
+        sc[blk] = dot * (lds_half_as_float(sb + 2u * (blk * 32 + tok)) * qstep);
+        if (masked) {
+          const int r = blk * 32 + tok;
+          if (s * TS + r >= seg.n || !((valid >> (r / 16)) & 1)) sc[blk] = kNegInf;
+        }
+      }
+
+      // ---- running maximum, weights, and their digits
+      int top = float_key(sc[0]);
+#pragma unroll
+      for (int blk = 1; blk < NBL; ++blk) top = max(top, float_key(sc[blk]));
+      const float mn = fmaxf(m, key_float(warp_max_s32(top)));
+      const float ref = mn == kNegInf ? 0.f : mn;
+      const float alpha = ex2(m - ref);
+      m = mn;
+      l *= alpha;
+      float wt[NBL], big = 0.f;
+#pragma unroll
+      for (int blk = 0; blk < NBL; ++blk) {
+        const float p = ex2(sc[blk] - ref);
+        l += p;
+        // a row that is masked weighs nothing whatever its scale holds
+        const float w = p * lds_half_as_float(sb + (uint32_t)TS * 2u + 2u * (blk * 32 + tok));
+        wt[blk] = p > 0.f ? w : 0.f;
+        big = __int_as_float(max(__float_as_int(big), __float_as_int(fabsf(wt[blk]))));
+      }
+      // Power-of-two scale that brings the largest weight to [2^21, 2^22).
+      const int bits = warp_max_s32(__float_as_int(big)), ex = max(22, bits >> 23);
+      const float up = __int_as_float((275 - ex) << 23);
+      // step; an infinite or NaN weight makes the result NaN
+      const float step = bits >= 0x7f800000 ? __int_as_float(0x7fffffff)
+                                            : __int_as_float((ex - 21) << 23) * (BITS == 4 ? 0.0625f : 1.f);
+#pragma unroll
+      for (int blk = 0; blk < NBL; ++blk)
+        sm_w[warp][blk * 32 + tok] = (uint32_t)(__float2int_rn(wt[blk] * up) + kDigitBias);
+      __syncwarp();
+
+      // ---- values
+      int acc[DG][4];
+#pragma unroll
+      for (int d = 0; d < DG; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0;
+#pragma unroll
+      for (int blk = 0; blk < NBL; ++blk) {
+        const uint4 w0 = *reinterpret_cast<const uint4*>(&sm_w[warp][blk * 32 + 4 * c4]);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(&sm_w[warp][blk * 32 + 16 + 4 * c4]);
+        const uint32_t b0 = (bytes_of(w0, wsel) ^ 0x80808080u) & wmask, b1 = (bytes_of(w1, wsel) ^ 0x80808080u) & wmask;
+#pragma unroll
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          uint32_t f[4];
+          ldsm_bytes_t(f, vb + lat_off<RB>(blk * 32 + lane, ch));
+          if constexpr (BITS == 8) {
+            imma32(acc[ch], f[0], f[1], f[2], f[3], b0, b1);
+          } else {
+            imma32(acc[2 * ch], (f[0] << 4) & 0xf0f0f0f0u, (f[1] << 4) & 0xf0f0f0f0u, (f[2] << 4) & 0xf0f0f0f0u,
+                   (f[3] << 4) & 0xf0f0f0f0u, b0, b1);
+            imma32(acc[2 * ch + 1], f[0] & 0xf0f0f0f0u, f[1] & 0xf0f0f0f0u, f[2] & 0xf0f0f0f0u, f[3] & 0xf0f0f0f0u, b0,
+                   b1);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DG; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] = fmaf((float)acc[d][i], step, o[d][i] * alpha);
+      __syncwarp();  // every lane has read this stage and the weights
+      stage = stage == S - 1 ? 0 : stage + 1;
+    }
+
+    // ---- the warp's result: digits joined (lanes c4 = 0 hold high and middle, 1 the low)
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (lane == 0) {
+      sm_m[warp] = m;
+      sm_l[warp] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DG; ++d)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float low = __shfl_down_sync(0xffffffffu, o[d][2 * half], 1);
+        const float v = fmaf(o[d][2 * half], 65536.f, fmaf(o[d][2 * half + 1], 256.f, low));
+        // latent column of operand row g + 8 half: int4 groups hold the even and the odd codes of a chunk
+        const int row = g + 8 * half;
+        const int j = BITS == 8 ? d * 16 + row : (d >> 1) * 32 + 2 * row + (d & 1);
+        if (c4 == 0) sm_o[warp][j] = v;
+      }
+    __syncthreads();
+    const bool whole = seg.s == 0 && seg.e == seg.strips();
+    constexpr int kSlot = R + 4;
+    float M = kNegInf, L = 0.f, sum = 0.f;
+    if (tid < R) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w]);
+      const float ref = M == kNegInf ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = ex2(sm_m[w] - ref);
+        L = fmaf(sm_l[w], f, L);
+        sum = fmaf(sm_o[w][tid], f, sum);
+      }
+    }
+    bool finish = whole;
+    if (!whole) {
+      float* part = a.partials + (size_t)(2 * c + (seg.s == 0 ? 1 : 0)) * kSlot;
+      if (tid < R) __stcg(part + tid, sum);
+      if (tid == 0) __stcg(reinterpret_cast<float2*>(part + R), make_float2(M, L));
+      int cf, np;
+      share.holders(seg, &cf, &np);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + bh, 1) == np - 1;
+      __syncthreads();
+      finish = sm_last;
+      if (finish) {
+        __threadfence();
+        if (tid < R) {  // in the order of the CTAs
+          const float* from = a.partials + (size_t)2 * cf * kSlot;
+          constexpr int kJoin = 8;
+          M = kNegInf;
+          L = sum = 0.f;
+          for (int i0 = 0; i0 < np; i0 += kJoin) {
+            float2 ml[kJoin];
+            float x[kJoin], mx = M;
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {
+              const float* p = from + (size_t)2 * (i0 + i) * kSlot + (i0 + i == 0 ? kSlot : 0);
+              const bool in = i0 + i < np;
+              ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + R)) : make_float2(kNegInf, 0.f);
+              x[i] = in ? __ldcg(p + tid) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) mx = fmaxf(mx, ml[i].x);
+            const float ref = mx == kNegInf ? 0.f : mx, f0 = ex2(M - ref);
+            L *= f0;
+            sum *= f0;
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {
+              const float f = ex2(ml[i].x - ref);
+              L = fmaf(ml[i].y, f, L);
+              sum = fmaf(x[i], f, sum);
+            }
+            M = mx;
+          }
+        }
+        if (tid == 0) st_relaxed_gpu(a.counters + bh, 0);
+      }
+    }
+    if (finish) {  // out = (o / L) . B_Vh, the latent columns spread over groups of Hd / 2 threads
+      if (tid < R) sm_res[tid] = sum / L;
+      __syncthreads();
+      const int pairs = Hd / 2, groups = C::kThreads / pairs, grp = tid / pairs, d2 = tid % pairs;
+      float2 v = make_float2(0.f, 0.f);
+      if (grp < groups) {
+        const __half2* bv = reinterpret_cast<const __half2*>(a.Bv + (size_t)h * R * Hd) + d2;
+#pragma unroll 4
+        for (int j = grp; j < R; j += groups) {
+          const float2 x = __half22float2(bv[(size_t)j * pairs]);
+          v.x = fmaf(sm_res[j], x.x, v.x);
+          v.y = fmaf(sm_res[j], x.y, v.y);
+        }
+        sm_up[grp * Hd + 2 * d2] = v.x;
+        sm_up[grp * Hd + 2 * d2 + 1] = v.y;
+      }
+      __syncthreads();
+      for (int d = tid; d < Hd; d += C::kThreads) {
+        float r = 0.f;
+        for (int i = 0; i < groups; ++i) r += sm_up[i * Hd + d];
+        a.out[bh * Hd + d] = r;
+      }
+    }
+    __syncthreads();  // the shared results are free again
+  }
+  cp_wait<0>();
+}
+
+struct LatKernel {
+  const void* fn;
+  size_t smem;
+  int threads;
+};
+template <int BITS, int RB>
+LatKernel lat_kernel() {
+  using C = LatCfg<BITS, RB>;
+  return LatKernel{reinterpret_cast<const void*>(&lat_decode_kernel<BITS, RB>), C::kSmem, C::kThreads};
+}
+bool pick_lat(int bits, int rowbytes, LatKernel* k) {
+  if (bits == 8) {
+    switch (rowbytes) {
+      case 16: *k = lat_kernel<8, 16>(); return true;
+      case 32: *k = lat_kernel<8, 32>(); return true;
+      case 64: *k = lat_kernel<8, 64>(); return true;
+      case 128: *k = lat_kernel<8, 128>(); return true;
+    }
+  } else {
+    switch (rowbytes) {
+      case 16: *k = lat_kernel<4, 16>(); return true;
+      case 32: *k = lat_kernel<4, 32>(); return true;
+      case 64: *k = lat_kernel<4, 64>(); return true;
+    }
+  }
+  return false;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
+
+}  // namespace
+
+extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits, int page_size, int num_pages,
+                                           int max_pages, const int32_t* seq_lens, const int32_t* block_table,
+                                           const void* q, int q_dtype, const uint8_t* lat_k, const uint8_t* lat_v,
+                                           const void* scale_k, const void* scale_v, const void* B_k, const void* B_v,
+                                           float softmax_scale, float* out, void* workspace, size_t workspace_bytes,
+                                           int32_t* err, void* stream) {
+  if (B < 0 || H < 1 || num_pages < 0 || max_pages < 0) return WSVD_ERR_INVALID_ARG;
+  if (B == 0) return WSVD_OK;
+  if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
+  if (r < 1 || (r * bits) % 8) return WSVD_ERR_INVALID_ARG;
+  if (q_dtype != WSVD_DTYPE_FP16 && q_dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
+  if (B > 4096 || (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256)) return WSVD_ERR_UNSUPPORTED;
+  const int shift = page_shift_of(page_size);
+  LatKernel kern;
+  if (shift < 0 || !pick_lat(bits, r * bits / 8, &kern)) return WSVD_ERR_UNSUPPORTED;
+  if ((long long)max_pages << shift > 0x7fffffffLL || (long long)B * H > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
+  if (!seq_lens || !block_table || !q || !lat_k || !lat_v || !scale_k || !scale_v || !B_k || !B_v || !out || !workspace)
+    return WSVD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(lat_k) || !aligned16(lat_v) || !aligned16(scale_k) || !aligned16(scale_v) ||
+      !aligned16(B_k) || !aligned16(B_v) || !aligned16(out) || !aligned16(workspace))
+    return WSVD_ERR_INVALID_ARG;
+  // The workspace of wsvd_decode_attention, laid out for this kernel: the
+  // counters where that call has them, so that calls of both may use it in turn.
+  const size_t counters = align16(((size_t)kMaxDecodeCtas + (size_t)B * H) * ((size_t)r + 2) * sizeof(float));
+  static_assert(2 * kMaxPagedCtas * 20 <= kMaxDecodeCtas * 18, "the partials of the smallest r fit before the counters");
+  if (workspace_bytes < wsvd_decode_workspace_size(B, H, r)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  LatDecodeArgs a{};
+  a.seqs = PagedSeqs{B, H, max_pages << shift, seq_lens};
+  a.H = H; a.Hd = Hd; a.page_shift = shift; a.num_pages = num_pages; a.max_pages = max_pages;
+  a.block_table = block_table;
+  a.lat_k = lat_k; a.lat_v = lat_v;
+  a.scale_k = static_cast<const __half*>(scale_k); a.scale_v = static_cast<const __half*>(scale_v);
+  a.Bv = static_cast<const __half*>(B_v);
+  a.out = out;
+  a.partials = reinterpret_cast<float*>(w);
+  a.counters = reinterpret_cast<int32_t*>(w + counters);
+  float* qglobal = reinterpret_cast<float*>(w + counters + align16((size_t)B * H * 4));
+  a.qglobal = qglobal;
+  a.err = err;
+  a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (paged_resident_ctas(kern.fn, kern.threads, kern.smem, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
+  // q' for every (b, h) first; the decode is launched behind it as its
+  // programmatic dependent and copies its first strips meanwhile.
+  if (launch_qproj(B, H, Hd, r, q, q_dtype, B_k, nullptr, 0, qglobal, s, false) != cudaSuccess) return WSVD_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.ctas);
+  cfg.blockDim = dim3((unsigned)kern.threads);
+  cfg.dynamicSmemBytes = kern.smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&a};
+  return cudaLaunchKernelExC(&cfg, kern.fn, args) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+}

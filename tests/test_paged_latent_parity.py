@@ -1,0 +1,196 @@
+"""GPU parity of the paged latent cache against the float64 oracle: the decode
+over pages of codes and scales, at the sizes and contents where it can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import rank_kv_cache_wsvd_b200 as W
+from oracle import paged_oracle as P
+from paged_util import cuda, f64, owned, randn, table_for
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from rank_kv_cache_wsvd_b200 import build
+    build.build()
+    W.load()
+
+
+def _cache(lens, H, r, bits, page, seed, caps=None, poison=True, **kw):
+    """Pages of random codes; rows of nobody hold arbitrary codes and NaN scales."""
+    table, pool = table_for(caps or lens, page, seed, **kw)
+    g = torch.Generator().manual_seed(seed)
+    mine = torch.from_numpy(owned(table, lens, page, pool))
+    out = []
+    for _ in range(2):
+        top = 127 if bits == 8 else 7
+        codes = torch.randint(-top, top + 1, (pool, H, page, r), generator=g, dtype=torch.int8)
+        if bits == 4:
+            codes = (codes[..., 0::2] & 15) | (codes[..., 1::2] << 4)
+        scale = ((torch.rand((pool, H, page), generator=g) + 0.5) / top).half()
+        if poison:
+            scale = scale.masked_fill(~mine[:, None], float("nan"))
+        out += [codes.view(torch.uint8).cuda(), scale.cuda()]
+    return out[0], out[2], out[1], out[3], table
+
+
+def _factors(H, r, Hd, seed):
+    return [(randn((H, r, Hd), "fp16", seed + i) * r ** -0.5).contiguous() for i in range(2)]
+
+
+def _decode(q, cache, Bk, Bv, lens, bits, **kw):
+    lk, lv, sk, sv, table = cache
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = W.wsvd_decode_attention_paged(q, lk, lv, sk, sv, Bk, Bv, cuda(table), cuda(np.asarray(lens, np.int32)), bits,
+                                        err=err, **kw)
+    torch.cuda.synchronize()
+    return out, int(err.item())
+
+
+def _check(out, q, cache, Bk, Bv, lens, bits, scale=None, what=""):
+    lk, lv, sk, sv, table = cache
+    z = [np.nan_to_num(f64(t)) for t in (sk, sv)]
+    ref, mass, wobble = P.latent_decode(f64(q), lk.cpu().numpy(), lv.cpu().numpy(), z[0], z[1], f64(Bk), f64(Bv), table,
+                                        lens, bits, scale)
+    # the largest value a row may add per column: full codes times the largest scale
+    big = z[1].max() * (127 if bits == 8 else 7) * np.abs(f64(Bv)).sum(1)[None]
+    n = max(max(lens), 1)
+    allow = P.latent_allowance(mass, wobble, Bk.shape[1], q.shape[-1], big, n)
+    got = out.double().cpu().numpy()
+    assert np.all(np.isfinite(got)), f"{what}: non-finite output"
+    worst = float((np.abs(got - ref) / allow).max())
+    assert worst <= 1.0, f"{what}: {worst:.3f}x the allowance, largest error {np.abs(got - ref).max():.3e}"
+
+
+LENS = [0, 1, 15, 16, 17, 31, 32, 33, 63, 65, 127, 128, 129, 300, 1, 0, 517]
+RANKS = [(8, 16), (8, 32), (8, 64), (8, 128), (4, 32), (4, 64), (4, 128)]
+
+
+@pytest.mark.parametrize("bits,r", RANKS)
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("Hd,dtype", [(32, "fp16"), (64, "bf16"), (128, "fp16"), (256, "bf16")])
+def test_latent_decode_ragged_lengths(bits, r, page, Hd, dtype):
+    H = 3
+    cache = _cache(LENS, H, r, bits, page, seed=r + bits)
+    Bk, Bv = _factors(H, r, Hd, 7)
+    q = randn((len(LENS), H, Hd), dtype, 9)
+    out, err = _decode(q, cache, Bk, Bv, LENS, bits)
+    assert err == 0
+    _check(out, q, cache, Bk, Bv, LENS, bits, what=f"int{bits} r{r} page{page} Hd{Hd}")
+
+
+@pytest.mark.parametrize("bits,r", RANKS)
+@pytest.mark.parametrize("B,H", [(1, 1), (2, 5), (70, 2)])
+def test_latent_decode_many_splits_and_many_sequences(bits, r, B, H):
+    lens = [6000 + 37 * b for b in range(B)] if B < 10 else [(b * 7) % 190 for b in range(B)]
+    cache = _cache(lens, H, r, bits, 32, seed=B + r)
+    Bk, Bv = _factors(H, r, 64, 17)
+    q = randn((B, H, 64), "bf16", 19)
+    out, err = _decode(q, cache, Bk, Bv, lens, bits)
+    assert err == 0
+    _check(out, q, cache, Bk, Bv, lens, bits, what=f"int{bits} r{r} B{B}")
+
+
+@pytest.mark.parametrize("scale", [0.02, 2.0, -0.3])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_latent_decode_softmax_scale(scale, bits):
+    lens = [200, 77]
+    cache = _cache(lens, 2, 32, bits, 64, seed=4)
+    Bk, Bv = _factors(2, 32, 128, 5)
+    q = randn((2, 2, 128), "fp16", 6)
+    out, err = _decode(q, cache, Bk, Bv, lens, bits, softmax_scale=scale)
+    assert err == 0
+    _check(out, q, cache, Bk, Bv, lens, bits, scale, f"scale {scale}")
+
+
+def test_latent_decode_extreme_codes_and_scales():
+    """Codes at -128 and -8, zero scales, scales over eight orders of magnitude,
+    zero and huge queries: the fixed-point sums neither overflow nor lose rows."""
+    for bits, r in ((8, 32), (4, 64)):
+        lens = [400, 260, 150]
+        cache = _cache(lens, 2, r, bits, 16, seed=3)
+        lk, lv, sk, sv, table = cache
+        lk[:, :, ::3] = 0x80 if bits == 8 else 0x88
+        lv[:, :, ::5] = 0x80 if bits == 8 else 0x88
+        sv[:, :, ::2] *= 2.0 ** -12
+        sv[:, 0, 1::4] *= 256
+        sk[:, :, ::7] = 0
+        Bk, Bv = _factors(2, r, 64, 8)
+        q = randn((3, 2, 64), "bf16", 9)
+        q[1] = 0
+        q[2] *= 64
+        out, err = _decode(q, cache, Bk, Bv, lens, bits)
+        assert err == 0
+        _check(out, q, cache, Bk, Bv, lens, bits, what=f"extreme int{bits}")
+
+
+def test_latent_decode_matches_the_contiguous_one():
+    """The same rows in pages and contiguous: both agree with the float64 value
+    under the framework's rule (1e-3 of the largest output, plus 1e-5)."""
+    from gpu_util import assert_attention_close
+    lens, H, Hd = [517, 64, 9], 4, 128
+    for bits, r in RANKS:
+        cache = _cache(lens, H, r, bits, 64, seed=77)
+        lk, lv, sk, sv, table = cache
+        Bk, Bv = _factors(H, r, Hd, 78)
+        q = randn((3, H, Hd), "fp16", 79)
+        flat = [torch.zeros((3, H, 520) + t.shape[3:], dtype=t.dtype, device="cuda") for t in (lk, lv, sk, sv)]
+        for b, m in enumerate(lens):
+            for l in range(m):
+                for to, t in zip(flat, (lk, lv, sk, sv)):
+                    to[b, :, l] = t[table[b, l // 64], :, l % 64]
+        n = cuda(np.asarray(lens, np.int32))
+        paged, err = _decode(q, cache, Bk, Bv, lens, bits)
+        dense = W.wsvd_decode_attention(q, flat[0], flat[1], flat[2], flat[3], Bk, Bv, n, bits)
+        assert err == 0
+        assert_attention_close(f64(paged).reshape(-1, Hd), f64(dense).reshape(-1, Hd), f"int{bits} r{r}")
+
+
+def test_latent_decode_bad_lengths_and_bad_pages():
+    lens = [50, 40, 64, 33]
+    cache = _cache(lens, 2, 32, 8, 16, seed=6, max_pages=4)
+    Bk, Bv = _factors(2, 32, 64, 7)
+    q = randn((4, 2, 64), "fp16", 8)
+    good, err = _decode(q, cache, Bk, Bv, lens, 8)
+    assert err == 0
+    for bad in (-1, 65, 2 ** 31 - 1, -2 ** 31):
+        out, err = _decode(q, cache, Bk, Bv, [50, bad, 64, 33], 8)
+        assert err == 1 and (out[1] == 0).all() and torch.equal(out[[0, 2, 3]], good[[0, 2, 3]])
+    for bad in (-1, cache[0].shape[0], 2 ** 31 - 1, -2 ** 31):
+        table = cache[4].copy()
+        table[2, 1] = bad
+        out, err = _decode(q, cache[:4] + (table,), Bk, Bv, lens, 8)
+        assert err == W.DEVERR_PAGE_RANGE and torch.equal(out[[0, 1, 3]], good[[0, 1, 3]])
+
+
+def test_latent_decode_repeats_its_bits_shares_the_contiguous_workspace_and_replays():
+    lens, H, r, Hd = [1900, 3, 700], 4, 32, 128
+    cache = _cache(lens, H, r, 8, 64, seed=12, caps=[1920] * 3)
+    Bk, Bv = _factors(H, r, Hd, 13)
+    q = randn((3, H, Hd), "bf16", 14)
+    want, _ = _decode(q, cache, Bk, Bv, lens, 8)
+    ws = W.workspace(W.wsvd_decode_workspace_size(3, H, r))
+    lk, lv, sk, sv, table = cache
+    flat = [torch.zeros((3, H, 64) + t.shape[3:], dtype=t.dtype, device="cuda") for t in (lk, lv, sk, sv)]
+    n3 = cuda(np.asarray([9, 64, 30], np.int32))
+    dense = W.wsvd_decode_attention(q, *flat, Bk, Bv, n3, 8)
+    for _ in range(3):
+        out, _ = _decode(q, cache, Bk, Bv, lens, 8, workspace_buf=ws)
+        assert torch.equal(out, want)
+        assert torch.equal(W.wsvd_decode_attention(q, *flat, Bk, Bv, n3, 8, workspace_buf=ws), dense)
+    tab, n = cuda(table), cuda(np.asarray(lens, np.int32))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = [W.wsvd_decode_attention_paged(q, lk, lv, sk, sv, Bk, Bv, tab, n, 8, stream=s) for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    out, graph = torch.empty_like(want), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        W.wsvd_decode_attention_paged(q, lk, lv, sk, sv, Bk, Bv, tab, n, 8, out=out, workspace_buf=ws)
+    for new in ([1900, 3, 700], [17, 0, 1], [640, 2, 129]):
+        n.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        want, _ = _decode(q, cache, Bk, Bv, new, 8)
+        assert torch.equal(out, want)
