@@ -534,6 +534,21 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  *   scale_k, scale_v [num_pages][H][page_size] fp16,
  * row by row the codes and scales of the contiguous cache.
  *
+ * wsvd_latent_append_paged: T new tokens per sequence, x [B][T][E], rotated,
+ * projected and quantised as by wsvd_latent_append, become rows seq_lens[b] ..
+ * seq_lens[b] + T - 1; seq_lens_out [B] (which may be seq_lens itself) receives
+ * the new lengths.  One token of at most 16 sequences runs as
+ * wsvd_latent_append does (the same codes and scales), any other block as
+ * wsvd_latent_prefill (likewise), with those calls' limits on E, r, B and
+ * hadamard_block (fp16 factors).
+ *   A sequence whose new rows do not fit in max_pages * page_size (or with
+ *   seq_lens[b] < 0) raises WSVD_DEVERR_CACHE_FULL, one that needs a bad page
+ *   WSVD_DEVERR_PAGE_RANGE; it is refused whole, its length kept.
+ *   workspace at least wsvd_latent_append_paged_workspace_size(B, T, E) bytes
+ *             whose first 256 are ZERO before the first call (every call leaves
+ *             them zero).  Calls sharing it must not overlap.
+ * T = 0 only copies the lengths.
+ *
  * wsvd_decode_attention_paged: the operation, arguments and results of
  * wsvd_decode_attention over the rows in the pages (one query per sequence and
  * latent head, fp16 factors).  Both products over the rows are exact integer
@@ -549,6 +564,12 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  *              not valid).
  * Rows >= seq_lens[b] are never used: their bytes may hold anything.  Two
  * launches.                                                                 */
+size_t wsvd_latent_append_paged_workspace_size(int B, int T, int E);
+int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int bits, int page_size, int num_pages, int max_pages,
+                             int hadamard_block, const void* x, int x_dtype, const void* A_k, const void* A_v,
+                             const int32_t* seq_lens, int32_t* seq_lens_out, const int32_t* block_table,
+                             uint8_t* lat_k, uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace,
+                             size_t workspace_bytes, int32_t* err, void* stream);
 int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits, int page_size, int num_pages, int max_pages,
                                 const int32_t* seq_lens, const int32_t* block_table, const void* q, int q_dtype,
                                 const uint8_t* lat_k, const uint8_t* lat_v, const void* scale_k, const void* scale_v,

@@ -68,6 +68,8 @@ SIGNATURES = {
     "paged_kv_append": (_c_int, [_c_int] * 11 + [_p, _c_ll] * 3 + [_c_int] + [_p] * 9 + [_c_size, _p, _p]),
     "paged_decode_workspace_size": (_c_size, [_c_int] * 5),
     "paged_decode_attention": (_c_int, [_c_int] * 8 + [_p] * 5 + [_c_int, _c_float, _p, _p, _c_size, _p, _p]),
+    "wsvd_latent_append_paged_workspace_size": (_c_size, [_c_int] * 3),
+    "wsvd_latent_append_paged": (_c_int, [_c_int] * 10 + [_p, _c_int] + [_p] * 10 + [_c_size, _p, _p]),
     "wsvd_decode_attention_paged": (_c_int, [_c_int] * 8 + [_p] * 3 + [_c_int] + [_p] * 6 + [_c_float, _p, _p, _c_size,
                                                                                               _p, _p]),
     "shared_latent_svd_decode": (_c_int, [_c_int] * 5 + [_p, _p, _c_int] + [_p] * 4 + [_c_float, _p, _p, _c_size,
@@ -458,6 +460,38 @@ def paged_decode_attention(q, k_pages, v_pages, block_table, seq_lens, softmax_s
 
 
 # ----------------------------------------------------------------------------- paged latent cache
+def wsvd_latent_append_paged_workspace_size(B, T, E) -> int:
+    return load().wsvd_latent_append_paged_workspace_size(B, T, E)
+
+
+def wsvd_latent_append_paged(x, A_k, A_v, seq_lens, block_table, lat_k, lat_v, scale_k, scale_v, bits: int,
+                             hadamard_block: int = 128, seq_lens_out=None, workspace_buf=None, err=None,
+                             stream=None) -> None:
+    """Quantise T new tokens per sequence (x [B][T][E]) into the pages that
+    block_table names, at rows seq_lens[b] .. ; lengths advance in place unless
+    seq_lens_out is given."""
+    lib = load()
+    B, T, E = shape = x.shape
+    H, _, r = A_k.shape
+    num_pages, _, page_size, rb = lat_k.shape
+    max_pages = block_table.shape[1]
+    dev, i32, f16, u8 = x.get_device(), torch.int32, torch.float16, torch.uint8
+    code = _dtype_code(x)
+    codes, scales, downs = (num_pages, H, page_size, r * bits // 8), (num_pages, H, page_size), (H, E, r)
+    pl = _dense(seq_lens, i32, (B,), dev, "seq_lens")
+    ws = _scratch(workspace_buf, dev, stream, lib.wsvd_latent_append_paged_workspace_size, B, T, E)
+    st = _launch(dev, lib.wsvd_latent_append_paged, B, T, H, E, r, bits, page_size, num_pages, max_pages, hadamard_block,
+                 _dense(x, x.dtype, shape, dev, "x"), code, _dense(A_k, f16, downs, dev, "A_k"),
+                 _dense(A_v, f16, downs, dev, "A_v"), pl,
+                 pl if seq_lens_out is None else _dense(seq_lens_out, i32, (B,), dev, "seq_lens_out"),
+                 _dense(block_table, i32, (B, max_pages), dev, "block_table"), _dense(lat_k, u8, codes, dev, "lat_k"),
+                 _dense(lat_v, u8, codes, dev, "lat_v"), _dense(scale_k, f16, scales, dev, "scale_k"),
+                 _dense(scale_v, f16, scales, dev, "scale_v"), ws.data_ptr(), ws.numel(),
+                 None if err is None else _dense(err, i32, err.shape, dev, "err"), _raw_stream(stream, dev))
+    if st:
+        _check(st, "wsvd_latent_append_paged")
+
+
 def wsvd_decode_attention_paged(q, lat_k, lat_v, scale_k, scale_v, B_k, B_v, block_table, seq_lens, bits: int,
                                 softmax_scale: float = 0.0, out=None, workspace_buf=None, err=None, stream=None):
     """wsvd_decode_attention over latents in pages: lat_k, lat_v

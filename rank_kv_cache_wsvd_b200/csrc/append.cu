@@ -32,6 +32,7 @@
 
 #include "append_core.cuh"
 #include "common.cuh"
+#include "paged_rows.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -64,10 +65,11 @@ static __host__ __device__ inline AppendSmem append_layout(int B, int Ec, int r,
   return s;
 }
 
-// R: the latent width, a compile-time constant of each instantiation.
-template <int BB, bool W8, int R>
-__device__ __forceinline__ void append_body(const AppendArgs& a, cg::cluster_group& cluster, uint8_t* smem,
-                                            const AppendSmem& L) {
+// R: the latent width, a compile-time constant of each instantiation.  PL: where
+// the rows lie (ContiguousRows or PagedRows).
+template <int BB, bool W8, int R, class PL>
+__device__ __forceinline__ void append_body(const AppendArgs& a, const PL& place, cg::cluster_group& cluster,
+                                            uint8_t* smem, const AppendSmem& L) {
   const int rank = (int)cluster.block_rank();
   const int unit = blockIdx.y, h = unit >> 1, kv = unit & 1;
   constexpr int r = R;
@@ -157,7 +159,7 @@ __device__ __forceinline__ void append_body(const AppendArgs& a, cg::cluster_gro
     if (prev == (int)gridDim.y - 1) {
       for (int b = 0; b < B; ++b) {
         const int pos = pos_sm[b];
-        if (pos >= 0 && pos < a.L_cap) st_relaxed_gpu(a.seq_lens + b, pos + 1);
+        place.advance(a.seq_lens, b, pos, 1, place.refused(b, pos, 1, a.L_cap) == 0);
       }
       st_relaxed_gpu(a.counter, 0);
     }
@@ -165,13 +167,14 @@ __device__ __forceinline__ void append_body(const AppendArgs& a, cg::cluster_gro
   const int RB = r * a.bits / 8;
   for (int b = warp; b < B; b += kAppendWarps) {
     const int pos = pos_sm[b];
-    const bool ok = pos >= 0 && pos < a.L_cap;
-    const size_t row = ((size_t)b * a.H + h) * a.L_cap + (ok ? pos : 0);
+    const int why = place.refused(b, pos, 1, a.L_cap);
+    const bool ok = why == 0;
+    const size_t row = ok ? place.row(b, h, a.H, pos, a.L_cap) : 0;
     const __half sh = quantise_append_row<W8, R>(slots + (size_t)b * r, (size_t)B * r, a.cluster, r, a.bits, a.hnorm,
                                                  cs, ok, (kv ? a.lat_v : a.lat_k) + row * RB, nullptr, lane);
     if (lane == 0) {
       if (ok) (kv ? a.scale_v : a.scale_k)[row] = sh;
-      else if (unit == 0) set_err(a.err, WSVD_DEVERR_CACHE_FULL);
+      else if (unit == 0) set_err(a.err, why);
     }
   }
 }
@@ -181,14 +184,14 @@ __device__ __forceinline__ void append_body(const AppendArgs& a, cg::cluster_gro
 // quantiser are fixed at compile time, and each kernel holds only its own
 // bodies (a kernel with every width's bodies measured instruction-fetch
 // stalls at thirteen cycles per issued instruction).
-template <bool W8, int R>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a) {
+template <bool W8, int R, class PL>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a, const PL place) {
   extern __shared__ __align__(128) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const AppendSmem L = append_layout(a.B, a.E / a.cluster, R, a.cluster);
-  if (a.B == 1) append_body<1, W8, R>(a, cluster, smem, L);
-  else if (a.B == 2) append_body<2, W8, R>(a, cluster, smem, L);
-  else append_body<4, W8, R>(a, cluster, smem, L);
+  if (a.B == 1) append_body<1, W8, R>(a, place, cluster, smem, L);
+  else if (a.B == 2) append_body<2, W8, R>(a, place, cluster, smem, L);
+  else append_body<4, W8, R>(a, place, cluster, smem, L);
 }
 
 int append_cluster_size(int E, int blk) {
@@ -201,17 +204,25 @@ size_t append_smem_bytes(int B, int E, int r, int cluster) {
   return append_layout(B, E / cluster, r, cluster).total;
 }
 
-cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
-  const size_t smem = append_smem_bytes(a.B, a.E, a.r, a.cluster);
-  void (*kern)(const AppendArgs) = nullptr;
-  switch (a.r) {
-    case 8: kern = a.w8 ? append_kernel<true, 8> : append_kernel<false, 8>; break;
-    case 16: kern = a.w8 ? append_kernel<true, 16> : append_kernel<false, 16>; break;
-    case 32: kern = a.w8 ? append_kernel<true, 32> : append_kernel<false, 32>; break;
-    case 64: kern = a.w8 ? append_kernel<true, 64> : append_kernel<false, 64>; break;
-    case 128: kern = a.w8 ? append_kernel<true, 128> : append_kernel<false, 128>; break;
-    default: return cudaErrorInvalidValue;  // rejected by the argument checks before this
+namespace {
+
+template <bool W8, class PL>
+auto pick_append(int r) -> void (*)(const AppendArgs, const PL) {
+  switch (r) {
+    case 8: return append_kernel<W8, 8, PL>;
+    case 16: return append_kernel<W8, 16, PL>;
+    case 32: return append_kernel<W8, 32, PL>;
+    case 64: return append_kernel<W8, 64, PL>;
+    case 128: return append_kernel<W8, 128, PL>;
+    default: return nullptr;
   }
+}
+
+template <class PL>
+cudaError_t launch_append_at(const AppendArgs& a, const PL& place, void (*kern)(const AppendArgs, const PL),
+                             cudaStream_t stream) {
+  const size_t smem = append_smem_bytes(a.B, a.E, a.r, a.cluster);
+  if (!kern) return cudaErrorInvalidValue;  // rejected by the argument checks before this
   {
     // Opt in to the dynamic shared memory once per device, kernel and size.
     static std::mutex mu;
@@ -242,7 +253,18 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.dep ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, a, place);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
+  return launch_append_at(a, ContiguousRows{},
+                          a.w8 ? pick_append<true, ContiguousRows>(a.r) : pick_append<false, ContiguousRows>(a.r), stream);
+}
+
+cudaError_t launch_append_paged(const AppendArgs& a, const PagedRows& place, cudaStream_t stream) {
+  return launch_append_at(a, place, pick_append<false, PagedRows>(a.r), stream);
 }
 
 }  // namespace wsvd

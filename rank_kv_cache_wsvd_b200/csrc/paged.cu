@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
       for (int i = tid; i < a.Tq * a.Hq * HD; i += C::kThreads) a.out[(size_t)b * a.Tq * a.Hq * HD + i] = 0.f;
   Strips<TS, kLead> share;
   typename Strips<TS, kLead>::Segment seg;
-  if (!share.deal(seqs, a.ctas, NW, a.err, &seg)) return;
+  if (!share.deal(seqs, c, a.ctas, NW, a.err, &seg)) return;
 
   // ---- the warp's copies: cursor `ld`, page ids one strip ahead
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;

@@ -6,7 +6,7 @@
 
 namespace wsvd {
 
-// ------------------------------------------------------------------ dealing strips to CTAs
+// ------------------------------------------------------------------ dealing strips to workers
 // The sequences of a call and their units: every sequence has `units` of them
 // (a head, or a head and a group of queries), each over all of its rows.
 struct PagedSeqs {
@@ -19,16 +19,17 @@ struct PagedSeqs {
 };
 
 // A unit's rows are cut into strips of TS rows, and counts as its strips plus
-// LEAD (what a segment costs beside its strips: queries, joins) when the CTAs'
-// shares are cut, else a CTA that meets many short sequences would finish last.
+// LEAD (what a segment costs beside its strips: queries, joins) when the shares
+// of the workers (CTAs or warps) are cut, else a worker that meets many short
+// sequences would finish last.
 template <int TS, int LEAD>
 struct Strips {
-  // The CTA's share of one unit: strips [s, e) of unit u of sequence b (n
+  // A worker's share of one unit: strips [s, e) of unit u of sequence b (n
   // rows); none when the share ends within the lead.
   struct Segment {
     int b, u, n, s, e;
     int at, taken;   // where the share begins in the unit (lead included), and how much of the unit it takes
-    long long left;  // of the CTA's share from here on
+    long long left;  // of the worker's share from here on
     __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
     __device__ __forceinline__ void enter(int place) {
       at = place;
@@ -51,26 +52,26 @@ struct Strips {
 
   static __device__ __forceinline__ int counted(int n) { return n > 0 ? (n + TS - 1) / TS + LEAD : 0; }
 
-  long long total, base, extra, end;  // strips in all; per CTA; CTAs with one more; this CTA's end
-  int ctas;                           // CTAs that have a share
+  long long total, base, extra, end;  // strips in all; per worker; workers with one more; this worker's end
+  int workers;                        // workers that have a share
 
   __device__ __forceinline__ long long begin_of(int c) const { return base * c + min((long long)c, extra); }
-  __device__ __forceinline__ int cta_of(long long strip) const {  // whose share holds a strip
+  __device__ __forceinline__ int worker_of(long long strip) const {  // whose share holds a strip
     const long long big = extra * (base + 1);
     return (int)(strip < big ? strip / (base + 1) : extra + (strip - big) / base);
   }
-  // The CTAs that hold strips of the segment's unit: the first, and how many.
+  // The workers that hold strips of the segment's unit: the first, and how many.
   __device__ __forceinline__ void holders(const Segment& g, int* first, int* count) const {
     const long long u0 = end - g.left - g.at + LEAD;  // the unit's first strip in the whole order
-    *first = cta_of(u0);
-    *count = cta_of(u0 + g.strips() - 1) - *first + 1;
+    *first = worker_of(u0);
+    *count = worker_of(u0 + g.strips() - 1) - *first + 1;
   }
 
-  // This CTA's share and its first segment; false when it has none.  Every warp
-  // finds it for itself (all lanes take part).  `least`: strips a CTA takes at
-  // least, so that a small problem is not cut too finely.
-  __device__ __forceinline__ bool deal(const PagedSeqs& q, int grid, int least, int32_t* err, Segment* seg) {
-    const int lane = threadIdx.x & 31, c = blockIdx.x;
+  // Worker c's share (of `count` workers) and its first segment; false when it
+  // has none.  Every warp finds it for itself (all lanes take part).  `least`:
+  // strips a worker takes at least, so that a small problem is not cut too finely.
+  __device__ __forceinline__ bool deal(const PagedSeqs& q, int c, int count, int least, int32_t* err, Segment* seg) {
+    const int lane = threadIdx.x & 31;
     const int per = (q.B + 31) / 32;
     const int b0 = min(q.B, lane * per), b1 = min(q.B, b0 + per);
     long long sum = 0;
@@ -89,10 +90,10 @@ struct Strips {
     const long long before = (incl - sum) * q.units;
     total = __shfl_sync(0xffffffffu, incl, 31) * q.units;
     const long long most = (total + least - 1) / least;
-    ctas = (int)(most < grid ? most : grid);
-    if (c >= ctas) return false;
-    base = (unsigned long long)total < 0x80000000ull ? (uint32_t)total / (uint32_t)ctas : total / ctas;
-    extra = total - base * ctas;
+    workers = (int)(most < count ? most : count);
+    if (c >= workers) return false;
+    base = (unsigned long long)total < 0x80000000ull ? (uint32_t)total / (uint32_t)workers : total / workers;
+    extra = total - base * workers;
     const long long begin = begin_of(c);
     end = begin + base + (c < extra ? 1 : 0);
     const bool mine = begin >= before && begin < before + sum * q.units;

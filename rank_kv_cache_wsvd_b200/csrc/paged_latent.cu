@@ -15,15 +15,22 @@
 // code (the contiguous decode) this takes most of the per-row work off the
 // issue slots, which bound that kernel for short rows.
 //
-// Work is dealt as in the dense paged decode: strips of rows over a grid of
-// CTAs, every warp its own cp.async pipeline, partial results of a head that
-// several CTAs share joined by the last of them.
+// Strips of rows are dealt evenly to warps.  Every warp is a worker of its own:
+// its cp.async pipeline, its running maximum and sum, its partial results, and
+// where it arrives last at a head, the join and the product with B_Vh.  Nothing
+// waits for a CTA, so one warp's joins are hidden by the others' strips (a
+// ragged int4 batch of 16 x 32 heads: 20.7 us; with the same pipelines joined per
+// CTA 30.0).  Measured, 32 heads: 4 x 32768 rows 33.8 / 50.9 / 89.9 / 172 us for
+// int8 r 16 / 32 / 64 / 128 (4.5 / 5.6 / 6.2 / 6.3 TB/s) and 40.0 / 54.2 / 96.0 for
+// int4 r 32 / 64 / 128; one sequence of 1600 rows 9.0 us.  Bound by HBM from 64-byte
+// rows on; shorter rows by the instructions a row costs whatever its length.
 #include <math.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "paged.cuh"
+#include "paged_rows.cuh"
 #include "wsvd_internal.h"
 
 using namespace wsvd;
@@ -42,16 +49,11 @@ struct LatCfg {
   static constexpr int kGroups = kTS / 16;                // of 16 rows, within one page each
   static constexpr int kHalf = kTS * RB;
   static constexpr int kStage = 2 * kHalf + 2 * kTS * 2;  // K codes, V codes, K scales, V scales
-#ifndef LT_WARPS
-#define LT_WARPS (RB == 16 ? 16 : 12)
-#endif
-#ifndef LT_STAGES
-#define LT_STAGES 2
-#endif
-#ifndef LT_LEAD
-#define LT_LEAD 24
-#endif
-  static constexpr int kWarps = LT_WARPS, kStages = LT_STAGES, kLead = LT_LEAD;
+  // Strips of 8 KB (4 KB for 16-byte rows): with strips of 64 rows instead of
+  // 128, 4 x 32768 rows of r 32 took 53.0 us (int8) and 46.3 (int4) against 50.9
+  // and 40.0.  A segment counts as two strips more (a ragged int4 batch of 16:
+  // 21.1 / 20.7 / 21.5 us with 1 / 2 / 4).
+  static constexpr int kWarps = 12, kStages = 2, kLead = 2;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kKS = kR >= 32 ? kR / 32 : 1;      // k steps of the score product
   static constexpr int kChunks = RB / 16;                 // 16-byte chunks of a row
@@ -68,7 +70,7 @@ struct LatDecodeArgs {
   const float* qglobal;  // [B][H][r]
   const __half* Bv;      // [H][r][Hd]
   float* out;
-  float* partials;       // [2 * ctas][r + 4]: o, then m, l
+  float* partials;       // [kMaxDecodeCtas + B * H][r + 2]: o, then m, l
   int32_t* counters;
   int32_t* err;
   float qscale;
@@ -121,25 +123,53 @@ __device__ __forceinline__ uint32_t bytes_of(const uint4& w, uint32_t sel) {
   return __byte_perm(__byte_perm(w.x, w.y, sel), __byte_perm(w.z, w.w, sel), 0x5410);
 }
 
+// A warp's out[0 .. 32 N) = (o . inv) . bv, bv [R][32 N] fp16; lane i columns N i ..
+template <int R, int N>
+__device__ __forceinline__ void up_project(const float* o, float inv, const __half* bv, float* out, int lane) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  constexpr int kFly = N == 8 ? 8 : 16;  // rows whose loads are in flight together
+#pragma unroll 1
+  for (int j0 = 0; j0 < R; j0 += kFly) {
+    __align__(16) __half x[kFly][N];
+#pragma unroll
+    for (int j = 0; j < kFly; ++j) {
+      const __half* p = bv + (size_t)(j0 + j) * 32 * N + lane * N;
+      if constexpr (N == 8) *reinterpret_cast<uint4*>(x[j]) = *reinterpret_cast<const uint4*>(p);
+      else if constexpr (N == 4) *reinterpret_cast<uint2*>(x[j]) = *reinterpret_cast<const uint2*>(p);
+      else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(x[j]) = *reinterpret_cast<const uint32_t*>(p);
+      else x[j][0] = *p;
+    }
+#pragma unroll
+    for (int j = 0; j < kFly; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = fmaf(o[j0 + j], __half2float(x[j][i]), v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[lane * N + i] = v[i] * inv;
+}
+
 template <int BITS, int RB>
 __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kernel(const LatDecodeArgs a) {
   using C = LatCfg<BITS, RB>;
   constexpr int TS = C::kTS, S = C::kStages, NW = C::kWarps, R = C::kR, KS = C::kKS, NBL = C::kBlocks, DG = C::kDG;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float sm_o[NW][R], sm_m[NW], sm_l[NW];
-  __shared__ __align__(16) uint32_t sm_w[NW][TS];
-  __shared__ float sm_res[R + 1], sm_up[C::kThreads * 2];
-  __shared__ int sm_valid[NW][S], sm_last;
+  __shared__ __align__(16) float sm_q[NW][R];      // q', then the result
+  __shared__ __align__(16) uint32_t sm_w[NW][TS];  // the strip's weights as digits
+  __shared__ int sm_valid[NW][S];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
-  const int c = blockIdx.x, H = a.H, Hd = a.Hd;
+  const int H = a.H, Hd = a.Hd;
   const PagedSeqs& seqs = a.seqs;
+  // Worker: one warp.  Few workers are spread over the SMs.
+  const int me = warp * gridDim.x + blockIdx.x;
 
-  for (int b = c; b < seqs.B; b += gridDim.x)
+  for (int b = blockIdx.x; b < seqs.B; b += gridDim.x)
     if (seqs.rows(b) == 0)
       for (int i = tid; i < H * Hd; i += C::kThreads) a.out[(size_t)b * H * Hd + i] = 0.f;
   Strips<TS, C::kLead> share;
   typename Strips<TS, C::kLead>::Segment seg;
-  if (!share.deal(seqs, a.ctas, NW, a.err, &seg)) {
+  if (!share.deal(seqs, me, min((int)gridDim.x * NW, kMaxDecodeCtas), 1, a.err, &seg)) {
     griddep_wait();  // the grid never completes before the q' grid it was launched behind
     return;
   }
@@ -147,14 +177,14 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
   // ---- the warp's copies: cursor `ld`; lane i holds the page of 16-row group i
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
   auto ld = seg;
-  int ls = ld.s + warp;
+  int ls = ld.s;
   bool more = true;
   int pg = -1;
   const int page_mask = (1 << a.page_shift) - 1;
   auto settle = [&]() {  // the next strip of this warp, and its pages
     while (more && ls >= ld.e) {
       more = ld.next(seqs);
-      ls = ld.s + warp;
+      ls = ld.s;
     }
     if (more) {
       const int l = ls * TS + lane * 16;
@@ -194,7 +224,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
         }
       }
       if (lane == 0) sm_valid[warp][stage] = valid;
-      ls += NW;
+      ++ls;
       settle();
     }
     cp_commit();
@@ -222,8 +252,14 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
     {
       const float* qg = a.qglobal + bh * R;
       float amax = 0.f;
-      for (int j = lane; j < R; j += 32) amax = fmaxf(amax, fabsf(__ldcg(qg + j)));
+#pragma unroll
+      for (int j0 = 0; j0 < R; j0 += 32) {
+        const float v = j0 + lane < R ? __ldcg(qg + j0 + lane) : 0.f;
+        if (j0 + lane < R) sm_q[warp][j0 + lane] = v;
+        amax = fmaxf(amax, fabsf(v));
+      }
       amax = key_float(warp_max_s32(float_key(amax)));
+      __syncwarp();
       const float inv = amax > 0.f ? (float)kDigitMax / amax : 0.f;
       qstep = amax / (float)kDigitMax * a.qscale * (BITS == 4 ? 0.0625f : 1.f);
 #pragma unroll
@@ -235,7 +271,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
           for (int i = 0; i < 4; ++i) {
             const int e = BITS == 8 ? k * 32 + x * 16 + 4 * c4 + i : k * 32 + 8 * c4 + 2 * i + x;
             int v = 0;
-            if (R >= 32 || x == 0) v = max(-kDigitMax, min(kDigitMax, __float2int_rn(__ldcg(qg + e) * inv)));
+            if (R >= 32 || x == 0) v = max(-kDigitMax, min(kDigitMax, __float2int_rn(sm_q[warp][e] * inv)));
             const uint32_t y = (uint32_t)(v + kDigitBias);
             hm |= ((y >> (g & 1 ? 8 : 16)) & 0xffu) << (8 * i);
             lo |= (y & 0xffu) << (8 * i);
@@ -249,7 +285,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
 #pragma unroll
     for (int d = 0; d < DG; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
 
-    for (int s = seg.s + warp; s < seg.e; s += NW) {
+    for (int s = seg.s; s < seg.e; ++s) {
       cp_wait<S - 2>();
       __syncwarp();
       issue(stage == 0 ? S - 1 : stage - 1);
@@ -371,13 +407,11 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
       stage = stage == S - 1 ? 0 : stage + 1;
     }
 
-    // ---- the warp's result: digits joined (lanes c4 = 0 hold high and middle, 1 the low)
+    // ---- the segment's result: digits joined (lanes c4 = 0 hold high and
+    // middle, 1 the low), lane j the latent columns j, j + 32, ...
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (lane == 0) {
-      sm_m[warp] = m;
-      sm_l[warp] = l;
-    }
+    __syncwarp();
 #pragma unroll
     for (int d = 0; d < DG; ++d)
 #pragma unroll
@@ -387,93 +421,76 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
         // latent column of operand row g + 8 half: int4 groups hold the even and the odd codes of a chunk
         const int row = g + 8 * half;
         const int j = BITS == 8 ? d * 16 + row : (d >> 1) * 32 + 2 * row + (d & 1);
-        if (c4 == 0) sm_o[warp][j] = v;
+        if (c4 == 0) sm_q[warp][j] = v;
       }
-    __syncthreads();
-    const bool whole = seg.s == 0 && seg.e == seg.strips();
-    constexpr int kSlot = R + 4;
-    float M = kNegInf, L = 0.f, sum = 0.f;
-    if (tid < R) {
+    __syncwarp();
+    constexpr int NJ = (R + 31) / 32, kSlot = R + 2;
+    if (seg.s != 0 || seg.e != seg.strips()) {
+      // Part of a unit: slot me + bh is this warp's alone, as workers and units
+      // both only rise along the shares.  The last to arrive joins the parts in
+      // the order of the workers, so the result does not depend on who that is.
+      int wf, np;
+      share.holders(seg, &wf, &np);
+      float* part = a.partials + ((size_t)me + bh) * kSlot;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w]);
-      const float ref = M == kNegInf ? 0.f : M;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float f = ex2(sm_m[w] - ref);
-        L = fmaf(sm_l[w], f, L);
-        sum = fmaf(sm_o[w][tid], f, sum);
-      }
-    }
-    bool finish = whole;
-    if (!whole) {
-      float* part = a.partials + (size_t)(2 * c + (seg.s == 0 ? 1 : 0)) * kSlot;
-      if (tid < R) __stcg(part + tid, sum);
-      if (tid == 0) __stcg(reinterpret_cast<float2*>(part + R), make_float2(M, L));
-      int cf, np;
-      share.holders(seg, &cf, &np);
+      for (int j0 = 0; j0 < R; j0 += 32)
+        if (j0 + lane < R) __stcg(part + j0 + lane, sm_q[warp][j0 + lane]);
+      if (lane == 0) __stcg(reinterpret_cast<float2*>(part + R), make_float2(m, l));
       __threadfence();
-      __syncthreads();
-      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + bh, 1) == np - 1;
-      __syncthreads();
-      finish = sm_last;
-      if (finish) {
-        __threadfence();
-        if (tid < R) {  // in the order of the CTAs
-          const float* from = a.partials + (size_t)2 * cf * kSlot;
-          constexpr int kJoin = 8;
-          M = kNegInf;
-          L = sum = 0.f;
-          for (int i0 = 0; i0 < np; i0 += kJoin) {
-            float2 ml[kJoin];
-            float x[kJoin], mx = M;
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) last = atom_add_acq_rel_gpu(a.counters + bh, 1) == np - 1;
+      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+      __threadfence();
+      const float* from = a.partials + ((size_t)wf + bh) * kSlot;
+      constexpr int kJoin = 8;  // partials whose loads are in flight together
+      float sum[NJ];
 #pragma unroll
-            for (int i = 0; i < kJoin; ++i) {
-              const float* p = from + (size_t)2 * (i0 + i) * kSlot + (i0 + i == 0 ? kSlot : 0);
-              const bool in = i0 + i < np;
-              ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + R)) : make_float2(kNegInf, 0.f);
-              x[i] = in ? __ldcg(p + tid) : 0.f;
-            }
+      for (int k = 0; k < NJ; ++k) sum[k] = 0.f;
+      m = kNegInf;
+      l = 0.f;
+      for (int i0 = 0; i0 < np; i0 += kJoin) {
+        float2 ml[kJoin];
+        float x[kJoin][NJ], mx = m;
 #pragma unroll
-            for (int i = 0; i < kJoin; ++i) mx = fmaxf(mx, ml[i].x);
-            const float ref = mx == kNegInf ? 0.f : mx, f0 = ex2(M - ref);
-            L *= f0;
-            sum *= f0;
+        for (int i = 0; i < kJoin; ++i) {
+          const float* p = from + (size_t)(i0 + i) * kSlot;
+          const bool in = i0 + i < np;
+          ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + R)) : make_float2(kNegInf, 0.f);
 #pragma unroll
-            for (int i = 0; i < kJoin; ++i) {
-              const float f = ex2(ml[i].x - ref);
-              L = fmaf(ml[i].y, f, L);
-              sum = fmaf(x[i], f, sum);
-            }
-            M = mx;
-          }
+          for (int k = 0; k < NJ; ++k) x[i][k] = in && k * 32 + lane < R ? __ldcg(p + k * 32 + lane) : 0.f;
         }
-        if (tid == 0) st_relaxed_gpu(a.counters + bh, 0);
-      }
-    }
-    if (finish) {  // out = (o / L) . B_Vh, the latent columns spread over groups of Hd / 2 threads
-      if (tid < R) sm_res[tid] = sum / L;
-      __syncthreads();
-      const int pairs = Hd / 2, groups = C::kThreads / pairs, grp = tid / pairs, d2 = tid % pairs;
-      float2 v = make_float2(0.f, 0.f);
-      if (grp < groups) {
-        const __half2* bv = reinterpret_cast<const __half2*>(a.Bv + (size_t)h * R * Hd) + d2;
-#pragma unroll 4
-        for (int j = grp; j < R; j += groups) {
-          const float2 x = __half22float2(bv[(size_t)j * pairs]);
-          v.x = fmaf(sm_res[j], x.x, v.x);
-          v.y = fmaf(sm_res[j], x.y, v.y);
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) mx = fmaxf(mx, ml[i].x);
+        const float ref = mx == kNegInf ? 0.f : mx, f0 = ex2(m - ref);
+        l *= f0;
+#pragma unroll
+        for (int k = 0; k < NJ; ++k) sum[k] *= f0;
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+          const float f = ex2(ml[i].x - ref);
+          l = fmaf(ml[i].y, f, l);
+#pragma unroll
+          for (int k = 0; k < NJ; ++k) sum[k] = fmaf(x[i][k], f, sum[k]);
         }
-        sm_up[grp * Hd + 2 * d2] = v.x;
-        sm_up[grp * Hd + 2 * d2 + 1] = v.y;
+        m = mx;
       }
-      __syncthreads();
-      for (int d = tid; d < Hd; d += C::kThreads) {
-        float r = 0.f;
-        for (int i = 0; i < groups; ++i) r += sm_up[i * Hd + d];
-        a.out[bh * Hd + d] = r;
-      }
+      if (lane == 0) st_relaxed_gpu(a.counters + bh, 0);
+#pragma unroll
+      for (int k = 0; k < NJ; ++k)
+        if (k * 32 + lane < R) sm_q[warp][k * 32 + lane] = sum[k];
+      __syncwarp();
     }
-    __syncthreads();  // the shared results are free again
+
+    // ---- out = (o / L) . B_Vh
+    const float inv = 1.f / l;
+    const __half* bv = a.Bv + (size_t)h * R * Hd;
+    float* out = a.out + bh * Hd;
+    if (Hd == 128) up_project<R, 4>(sm_q[warp], inv, bv, out, lane);
+    else if (Hd == 64) up_project<R, 2>(sm_q[warp], inv, bv, out, lane);
+    else if (Hd == 32) up_project<R, 1>(sm_q[warp], inv, bv, out, lane);
+    else up_project<R, 8>(sm_q[warp], inv, bv, out, lane);
+    __syncwarp();
   }
   cp_wait<0>();
 }
@@ -509,6 +526,29 @@ bool pick_lat(int bits, int rowbytes, LatKernel* k) {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 
+// Bytes in front of the prefill's scratch in the paged append's workspace: the
+// one-token append's completion counter, which every call leaves zero.
+constexpr size_t kPagedCounterBytes = 256;
+
+// Whether one token of each sequence can take the append's GEMV (the shapes
+// wsvd_latent_append takes), and its arguments.
+bool one_token_append(int B, int H, int E, int r, int bits, int cap, int hadamard_block, const void* x, int x_dtype,
+                      const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k, uint8_t* lat_v,
+                      void* scale_k, void* scale_v, void* counter, int32_t* err, AppendArgs* a) {
+  if (B > 16 || E > 65536 || (r != 8 && r != 16 && r != 32 && r != 64 && r != 128)) return false;
+  if (hadamard_block < 1 || hadamard_block > 1024 || (hadamard_block & (hadamard_block - 1)) || E % hadamard_block)
+    return false;
+  const int cl = append_cluster_size(E, hadamard_block);
+  if (cl < 1 || append_smem_bytes(B, E, r, cl) > 200 * 1024) return false;
+  a->B = B; a->H = H; a->E = E; a->r = r; a->bits = bits; a->L_cap = cap; a->blk = hadamard_block; a->cluster = cl;
+  a->hnorm = (float)(1.0 / sqrt((double)hadamard_block));
+  a->x = x; a->x_dtype = x_dtype; a->Ak = A_k; a->Av = A_v;
+  a->seq_lens = seq_lens; a->lat_k = lat_k; a->lat_v = lat_v;
+  a->scale_k = static_cast<__half*>(scale_k); a->scale_v = static_cast<__half*>(scale_v);
+  a->counter = static_cast<int32_t*>(counter); a->err = err;
+  return true;
+}
+
 }  // namespace
 
 extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits, int page_size, int num_pages,
@@ -535,7 +575,6 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   // The workspace of wsvd_decode_attention, laid out for this kernel: the
   // counters where that call has them, so that calls of both may use it in turn.
   const size_t counters = align16(((size_t)kMaxDecodeCtas + (size_t)B * H) * ((size_t)r + 2) * sizeof(float));
-  static_assert(2 * kMaxPagedCtas * 20 <= kMaxDecodeCtas * 18, "the partials of the smallest r fit before the counters");
   if (workspace_bytes < wsvd_decode_workspace_size(B, H, r)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   LatDecodeArgs a{};
@@ -570,4 +609,53 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   cfg.numAttrs = 1;
   void* args[] = {&a};
   return cudaLaunchKernelExC(&cfg, kern.fn, args) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+}
+
+extern "C" size_t wsvd_latent_append_paged_workspace_size(int B, int T, int E) {
+  return kPagedCounterBytes + wsvd_prefill_workspace_size(B, T, E);
+}
+
+extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int bits, int page_size, int num_pages,
+                                        int max_pages, int hadamard_block, const void* x, int x_dtype, const void* A_k,
+                                        const void* A_v, const int32_t* seq_lens, int32_t* seq_lens_out,
+                                        const int32_t* block_table, uint8_t* lat_k, uint8_t* lat_v, void* scale_k,
+                                        void* scale_v, void* workspace, size_t workspace_bytes, int32_t* err,
+                                        void* stream) {
+  if (B < 0 || T < 0 || H < 1 || E < 1 || r < 1 || num_pages < 0 || max_pages < 0) return WSVD_ERR_INVALID_ARG;
+  if (B == 0) return WSVD_OK;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || (long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
+  if (!seq_lens || !seq_lens_out || !block_table || !workspace) return WSVD_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return WSVD_ERR_INVALID_ARG;
+  if (seq_lens_out != seq_lens && overlap(seq_lens_out, (size_t)B * 4, seq_lens, (size_t)B * 4))
+    return WSVD_ERR_INVALID_ARG;
+  if (overlap(seq_lens_out, (size_t)B * 4, block_table, (size_t)B * max_pages * 4)) return WSVD_ERR_INVALID_ARG;
+  if (workspace_bytes < wsvd_latent_append_paged_workspace_size(B, T, E)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  const int cap = max_pages << shift;
+  const PagedRows place{block_table, max_pages, shift, num_pages, seq_lens_out};
+  int32_t* lens = const_cast<int32_t*>(seq_lens);  // read only: PagedRows writes seq_lens_out
+  if (T == 0) {
+    if (seq_lens_out != seq_lens &&
+        cudaMemcpyAsync(seq_lens_out, seq_lens, (size_t)B * 4, cudaMemcpyDeviceToDevice,
+                        reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return WSVD_ERR_CUDA;
+    return WSVD_OK;
+  }
+  if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
+  if (x_dtype != WSVD_DTYPE_FP16 && x_dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
+  if (!x || !A_k || !A_v || !lat_k || !lat_v || !scale_k || !scale_v) return WSVD_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(A_k) || !aligned16(A_v) || !aligned16(lat_k) || !aligned16(lat_v) ||
+      !aligned16(scale_k) || !aligned16(scale_v))
+    return WSVD_ERR_INVALID_ARG;
+  // One token of few sequences: the append's GEMV, bound by reading A once;
+  // blocks, and batches it does not take: the prefill's GEMM.
+  AppendArgs a{};
+  if (T == 1 && one_token_append(B, H, E, r, bits, cap, hadamard_block, x, x_dtype, A_k, A_v, lens, lat_k, lat_v,
+                                 scale_k, scale_v, workspace, err, &a)) {
+    (void)cudaGetLastError();
+    return launch_append_paged(a, place, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+  }
+  return prefill_paged(place, B, T, H, E, r, bits, cap, hadamard_block, x, x_dtype, A_k, A_v, lens, lat_k, lat_v, scale_k,
+                    scale_v, static_cast<uint8_t*>(workspace) + kPagedCounterBytes, workspace_bytes - kPagedCounterBytes,
+                    err, stream);
 }

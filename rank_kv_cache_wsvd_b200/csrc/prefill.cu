@@ -33,6 +33,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "paged_rows.cuh"
 #include "tc05.cuh"
 
 namespace wsvd {
@@ -329,7 +330,9 @@ __device__ __forceinline__ void load_stage(const PrefillArgs& a, const CopyPlan&
   for (int i = 0; i < kWPieces; ++i) cp_async16_zfill(st + p.w_dst[i], p.w[i] + (size_t)k0 * a.r, p.w_ok[i]);
 }
 
-__global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const PrefillArgs a) {
+// PL: where the rows lie (ContiguousRows or PagedRows).
+template <class PL>
+__global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const PrefillArgs a, const PL place) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __half* sm = reinterpret_cast<__half*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const Pre
     if (m >= a.M || n >= a.N) continue;  // warp-uniform
     const int b = m / a.T, t = m - b * a.T;
     const int pos = a.seq_lens[b];
-    if (pos < 0 || (long long)pos + a.T > a.L_cap) continue;  // refused block (flagged by the advance kernel)
+    if (place.refused(b, pos, a.T, a.L_cap)) continue;  // refused block (flagged by the advance kernel)
     const int kv = n / HR, h = (n - kv * HR) / a.r;
     const float ip = a.inv_p[m];
     float cv[4];
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const Pre
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
     const float sc = __half2float(sh);
-    const size_t row = ((size_t)b * a.H + h) * a.L_cap + pos + t;
+    const size_t row = place.row(b, h, a.H, pos + t, a.L_cap);
     uint8_t* dst = (kv ? a.lat_v : a.lat_k) + row * RB;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -548,11 +551,11 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
-template <int R, int BN_>
+template <int R, int BN_, class PL>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_xhi, const __grid_constant__ CUtensorMap tm_xlo,
                       const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
-                      const TcArgs a) {
+                      const TcArgs a, const PL place) {
   using C = TcCfg<R, BN_>;
   constexpr int BN = C::BN, NG = C::NG, S = kTcStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (m < a.M) {
       const int b = m / a.T, t = m - b * a.T;
       const int pos = a.seq_lens[b];
-      if (pos >= 0 && (long long)pos + a.T <= a.L_cap) {  // else refused (flagged by the advance kernel)
+      if (!place.refused(b, pos, a.T, a.L_cap)) {  // else flagged by the advance kernel
         const float ip = a.inv_p[m];
         const int Q = a.bits == 8 ? 127 : 7;
         constexpr int HEADS = BN / R < 1 ? 1 : BN / R;
@@ -700,7 +703,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
           const float sc = __half2float(sh);
-          const size_t crow = ((size_t)b * a.H + h) * a.L_cap + pos + t;
+          const size_t crow = place.row(b, h, a.H, pos + t, a.L_cap);
           if (a.bits == 8) {
             uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.lat_v : a.lat_k) + crow * R);
 #pragma unroll
@@ -785,15 +788,16 @@ bool encode_weight_map(CUtensorMap* tm, const void* base, int H, int E, int r, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int R, int BN>
-cudaError_t launch_tc(const PrefillArgs& pa, const void* A_k, const void* A_v, int32_t* err, cudaStream_t s) {
+template <int R, int BN, class PL>
+cudaError_t launch_tc(const PrefillArgs& pa, const PL& place, const void* A_k, const void* A_v, int32_t* err,
+                      cudaStream_t s) {
   using C = TcCfg<R, BN>;
   CUtensorMap mh, ml, mk, mv;
   if (!encode_act_map(&mh, pa.xhi, pa.M, pa.E) || !encode_act_map(&ml, pa.xlo, pa.M, pa.E) ||
       !encode_weight_map(&mk, A_k, pa.H, pa.E, R, C::NG) || !encode_weight_map(&mv, A_v, pa.H, pa.E, R, C::NG))
     return cudaErrorInvalidValue;
   cudaError_t e =
-      cudaFuncSetAttribute(prefill_tc_kernel<R, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      cudaFuncSetAttribute(prefill_tc_kernel<R, BN, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   TcArgs ta{};
   ta.M = pa.M; ta.T = pa.T; ta.H = pa.H; ta.bits = pa.bits; ta.L_cap = pa.L_cap; ta.KT = pa.E / kTcBK;
@@ -811,7 +815,7 @@ cudaError_t launch_tc(const PrefillArgs& pa, const void* A_k, const void* A_v, i
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<R, BN>, mh, ml, mk, mv, ta);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<R, BN, PL>, mh, ml, mk, mv, ta, place);
 }
 
 // Output tile width of the tcgen05 path: 128 columns when the tiles hold whole
@@ -828,33 +832,26 @@ int tc_tile_width(long long M, int H, int r) {
 }
 
 // ------------------------------------------------------------------ 3. lengths
-__global__ void prefill_advance_kernel(int32_t* seq_lens, int B, int T, int L_cap, int32_t* err) {
+template <class PL>
+__global__ void prefill_advance_kernel(int32_t* seq_lens, int B, int T, int L_cap, const PL place, int32_t* err) {
   griddep_wait();  // launched as a programmatic dependent of the GEMM, which reads the lengths
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
     const int pos = seq_lens[b];
-    if (pos >= 0 && (long long)pos + T <= L_cap) seq_lens[b] = pos + T;
-    else set_err(err, WSVD_DEVERR_CACHE_FULL);
+    const int why = place.refused(b, pos, T, L_cap);
+    place.advance(seq_lens, b, pos, T, why == 0);
+    if (why) set_err(err, why);
   }
 }
 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-}  // namespace
-
-}  // namespace wsvd
-
-extern "C" size_t wsvd_prefill_workspace_size(int B, int T, int E) {
-  if (B < 1 || T < 1 || E < 1) return 0;
-  const size_t M = (size_t)B * T;
-  return 2 * wsvd::align16(M * E * 2) + wsvd::align16(M * 4);
-}
-
-extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
-                                   const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens,
-                                   uint8_t* lat_k, uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace,
-                                   size_t workspace_bytes, int32_t* err, void* stream) {
-  using namespace wsvd;
+// wsvd_latent_prefill's checks and launches for rows that lie as `place` says.
+template <class PL>
+int prefill_at(const PL& place, int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
+               const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k,
+               uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace, size_t workspace_bytes, int32_t* err,
+               void* stream) {
   if (B < 0 || T < 0 || H < 1 || E < 1 || r < 1 || L_cap < 0) return WSVD_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return WSVD_OK;
   if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
@@ -890,7 +887,7 @@ extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, 
   const size_t rot_smem = (size_t)E * 4;
   if (cudaFuncSetAttribute(prefill_rotate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rot_smem) !=
           cudaSuccess ||
-      cudaFuncSetAttribute(prefill_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem) !=
+      cudaFuncSetAttribute(prefill_gemm_kernel<PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem) !=
           cudaSuccess)
     return WSVD_ERR_CUDA;
   const float hnorm = (float)(1.0 / sqrt((double)hadamard_block));
@@ -925,22 +922,22 @@ extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, 
     cudaError_t e = cudaSuccess;
     if (bn == 128) {
       switch (r) {
-        case 16: e = launch_tc<16, 128>(a, A_k, A_v, err, s); break;
-        case 32: e = launch_tc<32, 128>(a, A_k, A_v, err, s); break;
-        case 64: e = launch_tc<64, 128>(a, A_k, A_v, err, s); break;
-        default: e = launch_tc<128, 128>(a, A_k, A_v, err, s); break;
+        case 16: e = launch_tc<16, 128>(a, place, A_k, A_v, err, s); break;
+        case 32: e = launch_tc<32, 128>(a, place, A_k, A_v, err, s); break;
+        case 64: e = launch_tc<64, 128>(a, place, A_k, A_v, err, s); break;
+        default: e = launch_tc<128, 128>(a, place, A_k, A_v, err, s); break;
       }
     } else {
       switch (r) {
-        case 16: e = launch_tc<16, 64>(a, A_k, A_v, err, s); break;
-        case 32: e = launch_tc<32, 64>(a, A_k, A_v, err, s); break;
-        default: e = launch_tc<64, 64>(a, A_k, A_v, err, s); break;
+        case 16: e = launch_tc<16, 64>(a, place, A_k, A_v, err, s); break;
+        case 32: e = launch_tc<32, 64>(a, place, A_k, A_v, err, s); break;
+        default: e = launch_tc<64, 64>(a, place, A_k, A_v, err, s); break;
       }
     }
     if (e != cudaSuccess) return WSVD_ERR_CUDA;
   } else {
     const dim3 grid((unsigned)((M + kBM - 1) / kBM), (unsigned)((N + kBN - 1) / kBN));
-    prefill_gemm_kernel<<<grid, kGemmThreads, kGemmSmem, s>>>(a);
+    prefill_gemm_kernel<PL><<<grid, kGemmThreads, kGemmSmem, s>>>(a, place);
   }
   {
     cudaLaunchAttribute attr[1];
@@ -952,8 +949,34 @@ extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, prefill_advance_kernel, seq_lens, B, T, L_cap, err) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, prefill_advance_kernel<PL>, seq_lens, B, T, L_cap, place, err) != cudaSuccess)
       return WSVD_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+}
+
+}  // namespace
+
+int prefill_paged(const PagedRows& place, int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
+                  const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k,
+                  uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace, size_t workspace_bytes, int32_t* err,
+                  void* stream) {
+  return prefill_at(place, B, T, H, E, r, bits, L_cap, hadamard_block, x, x_dtype, A_k, A_v, seq_lens, lat_k, lat_v,
+                    scale_k, scale_v, workspace, workspace_bytes, err, stream);
+}
+
+}  // namespace wsvd
+
+extern "C" size_t wsvd_prefill_workspace_size(int B, int T, int E) {
+  if (B < 1 || T < 1 || E < 1) return 0;
+  const size_t M = (size_t)B * T;
+  return 2 * wsvd::align16(M * E * 2) + wsvd::align16(M * 4);
+}
+
+extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
+                                   const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens,
+                                   uint8_t* lat_k, uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace,
+                                   size_t workspace_bytes, int32_t* err, void* stream) {
+  return wsvd::prefill_at(wsvd::ContiguousRows{}, B, T, H, E, r, bits, L_cap, hadamard_block, x, x_dtype, A_k, A_v,
+                          seq_lens, lat_k, lat_v, scale_k, scale_v, workspace, workspace_bytes, err, stream);
 }

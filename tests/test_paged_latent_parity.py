@@ -194,3 +194,175 @@ def test_latent_decode_repeats_its_bits_shares_the_contiguous_workspace_and_repl
         graph.replay()
         want, _ = _decode(q, cache, Bk, Bv, new, 8)
         assert torch.equal(out, want)
+
+
+# ----------------------------------------------------------------------------- append
+def _x(B, T, E, seed, dtype="bf16"):
+    return randn((B, T, E), dtype, seed)
+
+
+def _down(H, E, r, seed):
+    return [(randn((H, E, r), "fp16", seed + i) * E ** -0.5).contiguous() for i in range(2)]
+
+
+def _empty(pool, H, r, bits, page, seed):
+    g = torch.Generator().manual_seed(seed)
+    lat = [torch.randint(0, 256, (pool, H, page, r * bits // 8), generator=g, dtype=torch.uint8).cuda() for _ in range(2)]
+    return lat + [torch.rand((pool, H, page), generator=g).half().cuda() for _ in range(2)]
+
+
+def _contiguous_rows(x, Ak, Av, lens, bits, blk, one):
+    """Codes and scales that the contiguous calls write for x, [B][H][T][..]."""
+    B, T, E = x.shape
+    H, _, r = Ak.shape
+    cap = (max(lens) + T + 7) // 8 * 8
+    lat = [torch.zeros((B, H, cap, r * bits // 8), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    sc = [torch.zeros((B, H, cap), dtype=torch.float16, device="cuda") for _ in range(2)]
+    n = cuda(np.asarray(lens, np.int32))
+    if one:
+        W.wsvd_latent_append(x[:, 0].contiguous(), Ak, Av, n, *lat, *sc, bits, blk)
+    else:
+        W.wsvd_latent_prefill(x, Ak, Av, n, *lat, *sc, bits, blk)
+    return [torch.stack([t[b, :, lens[b]:lens[b] + T] for b in range(B)]) for t in lat + sc]
+
+
+@pytest.mark.parametrize("bits,r", [(8, 8), (8, 16), (8, 32), (8, 64), (8, 128), (4, 8), (4, 32), (4, 128)])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("B,T,H,E,blk", [(1, 1, 4, 256, 128), (5, 1, 3, 512, 64), (20, 1, 4, 256, 128),
+                                         (3, 37, 4, 256, 128), (2, 130, 3, 192, 1)])
+def test_latent_append_writes_the_contiguous_calls_rows(bits, r, page, B, T, H, E, blk):
+    """Row for row the codes and scales of wsvd_latent_append (one token of up to
+    16 sequences) or wsvd_latent_prefill; every other row of the pool keeps its
+    bytes."""
+    lens = [(b * 29) % 70 for b in range(B)]
+    table, pool = table_for([a + T for a in lens], page, seed=r + B)
+    lk, lv, sk, sv = _empty(pool, H, r, bits, page, 5)
+    before = [t.clone() for t in (lk, lv, sk, sv)]
+    x, (Ak, Av) = _x(B, T, E, 6), _down(H, E, r, 7)
+    n = cuda(np.asarray(lens, np.int32))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    W.wsvd_latent_append_paged(x, Ak, Av, n, cuda(table), lk, lv, sk, sv, bits, blk, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and n.tolist() == [a + T for a in lens]
+    want = _contiguous_rows(x, Ak, Av, lens, bits, blk, T == 1 and B <= 16)
+    for got, old, rows in zip((lk, lv, sk, sv), before, want):
+        for b in range(B):
+            for t in range(T):
+                l = lens[b] + t
+                old[table[b, l // page], :, l % page] = rows[b, :, t]
+        assert torch.equal(got.view(torch.uint8), old.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("B,T", [(2, 1), (2, 9)])
+def test_latent_append_against_the_oracle(bits, B, T):
+    """Codes and scales against the float64 oracle's append, token by token, with
+    the framework's counted-tie rule."""
+    import oracle as O
+    from gpu_util import compare_codes, unpack
+    H, E, r, page, blk = 4, 256, 32, 16, 128
+    lens = [15, 3]
+    table, pool = table_for([a + T for a in lens], page, seed=3)
+    lk, lv, sk, sv = _empty(pool, H, r, bits, page, 5)
+    x, (Ak, Av) = _x(B, T, E, 16), _down(H, E, r, 17)
+    W.wsvd_latent_append_paged(x, Ak, Av, cuda(np.asarray(lens, np.int32)), cuda(table), lk, lv, sk, sv, bits, blk)
+    cap = 32
+    ol, os_ = [np.zeros((B, H, cap, r * bits // 8), np.uint8) for _ in range(2)], \
+        [np.zeros((B, H, cap), np.float16) for _ in range(2)]
+    n, cs = np.asarray(lens, np.int32), []
+    for t in range(T):
+        k, s_k, v, s_v, n, _, ck, cv = O.latent_append(x[:, t].float().cpu().numpy(), Ak.cpu().numpy(), Av.cpu().numpy(),
+                                                       n, ol[0], os_[0], ol[1], os_[1], r, bits, blk)
+        ol, os_ = [k, v], [s_k, s_v]
+        cs.append((ck, cv))
+    ties = 0
+    for kv, (lat, sc) in enumerate(((lk, sk), (lv, sv))):
+        for t in range(T):
+            got_c = np.stack([unpack(lat[table[b, (lens[b] + t) // page], :, (lens[b] + t) % page].cpu().numpy(), r, bits)
+                              for b in range(B)])
+            got_s = np.stack([sc[table[b, (lens[b] + t) // page], :, (lens[b] + t) % page].cpu().numpy() for b in range(B)])
+            want_c = np.stack([unpack(ol[kv][b, :, lens[b] + t], r, bits) for b in range(B)])
+            want_s = np.stack([os_[kv][b, :, lens[b] + t] for b in range(B)])
+            a, b_ = compare_codes(got_c, got_s, want_c, want_s, cs[t][kv], bits)
+            ties += a + b_
+    assert ties <= 2 + 2 * B * T * H * r * 4e-3
+
+
+def test_latent_append_refuses_sequences_whole():
+    for T in (1, 20):
+        H, E, r, page = 2, 256, 16, 16
+        lens = [0, 64 - T + 1, -1, 31, 2 ** 31 - 1, 5]
+        table, pool = table_for([64] * 6, page, 5)
+        table[3, 1 if T == 1 else 2] = pool + 4
+        lk, lv, sk, sv = _empty(pool, H, r, 8, page, 8)
+        before = [t.clone() for t in (lk, lv, sk, sv)]
+        x, (Ak, Av) = _x(6, T, E, 9), _down(H, E, r, 10)
+        n = cuda(np.asarray(lens, np.int32))
+        to = torch.full_like(n, -7)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        W.wsvd_latent_append_paged(x, Ak, Av, n, cuda(table), lk, lv, sk, sv, 8, 128, seq_lens_out=to, err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 2 | 8
+        assert n.tolist() == lens and to.tolist() == [T] + lens[1:5] + [5 + T]
+        for b in (0, 5):
+            rows = _contiguous_rows(x[b:b + 1].contiguous(), Ak, Av, [lens[b]], 8, 128, T == 1)
+            for t in range(T):
+                l = lens[b] + t
+                for old, new in zip(before, rows):
+                    old[table[b, l // page], :, l % page] = new[0, :, t]
+        for got, old in zip((lk, lv, sk, sv), before):
+            assert torch.equal(got.view(torch.uint8), old.view(torch.uint8))
+
+
+def test_latent_append_and_decode_as_used():
+    """A prompt block, then one token at a time through one workspace; every
+    output against the oracle over the pages' codes, the codes against the
+    contiguous calls; then captured steps."""
+    import oracle as O  # noqa: F401
+    B, H, E, r, Hd, page, bits, T = 3, 4, 512, 32, 64, 16, 8, 40
+    table, pool = table_for([64] * B, page, 9)
+    lk, lv, sk, sv = _empty(pool, H, r, bits, page, 11)
+    tab, n = cuda(table), torch.zeros(B, dtype=torch.int32, device="cuda")
+    Ak, Av = _down(H, E, r, 12)
+    Bk, Bv = _factors(H, r, Hd, 14)
+    ws = W.workspace(W.wsvd_latent_append_paged_workspace_size(B, T, E))
+    dws = W.workspace(W.wsvd_decode_workspace_size(B, H, r))
+    lens = [0] * B
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i, t in enumerate([T] + [1] * 5):
+        x, q = _x(B, t, E, 20 + i), randn((B, H, Hd), "bf16", 40 + i)
+        W.wsvd_latent_append_paged(x, Ak, Av, n, tab, lk, lv, sk, sv, bits, 128, workspace_buf=ws, err=err)
+        rows = _contiguous_rows(x, Ak, Av, lens, bits, 128, t == 1)
+        for b in range(B):
+            l = lens[b] + t - 1
+            assert torch.equal(lk[table[b, l // page], :, l % page], rows[0][b, :, -1])
+            assert torch.equal(sv[table[b, l // page], :, l % page], rows[3][b, :, -1])
+        lens = [a + t for a in lens]
+        out = W.wsvd_decode_attention_paged(q, lk, lv, sk, sv, Bk, Bv, tab, n, bits, workspace_buf=dws, err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and n.tolist() == lens
+        _check(out, q, (lk, lv, sk, sv, table), Bk, Bv, lens, bits, what=f"step {i}")
+    x, q, out = _x(B, 1, E, 60), randn((B, H, Hd), "bf16", 61), torch.empty((B, H, Hd), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        W.wsvd_latent_append_paged(x, Ak, Av, n, tab, lk, lv, sk, sv, bits, 128, workspace_buf=ws, err=err)
+        W.wsvd_decode_attention_paged(q, lk, lv, sk, sv, Bk, Bv, tab, n, bits, out=out, workspace_buf=dws, err=err)
+    for i in range(3):
+        x.copy_(_x(B, 1, E, 70 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        lens = [a + 1 for a in lens]
+        assert int(err.item()) == 0 and n.tolist() == lens
+        _check(out, q, (lk, lv, sk, sv, table), Bk, Bv, lens, bits, what=f"replay {i}")
+    assert (ws[:256] == 0).all()
+
+
+def test_latent_append_of_no_tokens_copies_the_lengths():
+    H, E, r, page = 2, 256, 16, 16
+    table, pool = table_for([64] * 2, page, 5)
+    lk, lv, sk, sv = _empty(pool, H, r, 8, page, 8)
+    Ak, Av = _down(H, E, r, 10)
+    n, to = cuda(np.asarray([5, 9], np.int32)), torch.zeros(2, dtype=torch.int32, device="cuda")
+    W.wsvd_latent_append_paged(torch.empty((2, 0, E), dtype=torch.bfloat16, device="cuda"), Ak, Av, n, cuda(table), lk, lv,
+                               sk, sv, 8, 128, seq_lens_out=to)
+    assert to.tolist() == [5, 9]
