@@ -537,10 +537,14 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  * wsvd_latent_append_paged: T new tokens per sequence, x [B][T][E], rotated,
  * projected and quantised as by wsvd_latent_append, become rows seq_lens[b] ..
  * seq_lens[b] + T - 1; seq_lens_out [B] (which may be seq_lens itself) receives
- * the new lengths.  One token of at most 16 sequences runs as
- * wsvd_latent_append does (the same codes and scales), any other block as
- * wsvd_latent_prefill (likewise), with those calls' limits on E, r, B and
- * hadamard_block (fp16 factors).
+ * the new lengths (fp16 factors).
+ *   One token of up to 4 sequences takes wsvd_latent_append's kernel and gives
+ *   its codes and scales bit for bit; so does one token of up to 16 sequences
+ *   where E is no multiple of 64 or above 16384, with that call's limits.
+ *   Everything else takes wsvd_latent_prefill's kernels, with that call's
+ *   limits on E, r, hadamard_block and B * T; when the block is small a
+ *   cluster of CTAs splits E, so that a code or scale on a rounding border may
+ *   differ from the contiguous call's.
  *   A sequence whose new rows do not fit in max_pages * page_size (or with
  *   seq_lens[b] < 0) raises WSVD_DEVERR_CACHE_FULL, one that needs a bad page
  *   WSVD_DEVERR_PAGE_RANGE; it is refused whole, its length kept.

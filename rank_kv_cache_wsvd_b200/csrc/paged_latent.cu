@@ -530,6 +530,14 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 // one-token append's completion counter, which every call leaves zero.
 constexpr size_t kPagedCounterBytes = 256;
 
+// Sequences up to which one token each takes the append's GEMV (fp32 FMAs, up to
+// four tokens per pass over the weights) rather than the GEMM.  Measured with
+// 32 heads, E 4096, GEMV / GEMM in us: r 32, 1 / 4 / 8 / 16 sequences 6.8 / 12.3 /
+// 26.7 / 78.3 against 17.7 / 17.9 / 18.5 / 18.7; r 64 9.2 / 22.4 / 40.7 against
+// 23.0 / 25.9 / 20.8; 8 heads of r 32 5.3 / 7.8 / 13.5 / 39.8 against 13.7 / 13.8 /
+// 14.1 / 14.6.
+constexpr int kGemvTokens = 4;
+
 // Whether one token of each sequence can take the append's GEMV (the shapes
 // wsvd_latent_append takes), and its arguments.
 bool one_token_append(int B, int H, int E, int r, int bits, int cap, int hadamard_block, const void* x, int x_dtype,
@@ -647,10 +655,11 @@ extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int b
   if (!aligned16(x) || !aligned16(A_k) || !aligned16(A_v) || !aligned16(lat_k) || !aligned16(lat_v) ||
       !aligned16(scale_k) || !aligned16(scale_v))
     return WSVD_ERR_INVALID_ARG;
-  // One token of few sequences: the append's GEMV, bound by reading A once;
-  // blocks, and batches it does not take: the prefill's GEMM.
+  // One token of few sequences, and of up to 16 where E does not suit the GEMM:
+  // the append's GEMV, bound by reading A once; all else the prefill's GEMM.
   AppendArgs a{};
-  if (T == 1 && one_token_append(B, H, E, r, bits, cap, hadamard_block, x, x_dtype, A_k, A_v, lens, lat_k, lat_v,
+  const bool gemm = E % 64 == 0 && E <= 16384;
+  if (T == 1 && (B <= kGemvTokens || !gemm) && one_token_append(B, H, E, r, bits, cap, hadamard_block, x, x_dtype, A_k, A_v, lens, lat_k, lat_v,
                                  scale_k, scale_v, workspace, err, &a)) {
     (void)cudaGetLastError();
     return launch_append_paged(a, place, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;

@@ -8,6 +8,7 @@
 namespace wsvd {
 
 struct ContiguousRows {
+  static constexpr bool kSplits = false;  // the prefill's tiles are never split over E: its rows keep their bits
   // 0, or the WSVD_DEVERR_* bit for which rows pos .. pos + n - 1 of sequence b are refused.
   __device__ __forceinline__ int refused(int, int pos, int n, int L_cap) const {
     return pos >= 0 && (long long)pos + n <= L_cap ? 0 : WSVD_DEVERR_CACHE_FULL;
@@ -24,6 +25,7 @@ struct ContiguousRows {
 
 // L_cap is the page table's capacity max_pages << page_shift.
 struct PagedRows {
+  static constexpr bool kSplits = true;
   const int32_t* block_table;  // [B][max_pages]
   int max_pages, page_shift, num_pages;
   int32_t* seq_lens_out;       // receives every length
