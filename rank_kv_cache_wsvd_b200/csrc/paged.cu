@@ -694,6 +694,10 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Queries per chunk: two column blocks of 8, one at head size 256 (registers).
+// Four blocks at head sizes 32 and 64, which read the rows once for 32 queries,
+// gave nothing (28 queries, 9 x 32768 rows of 4 heads of 64: 97.0 us against
+// 98.8; 9 ragged sequences 26.4 against 24.3): the products bound these, not the
+// second read of the rows from L2.
 inline int chunk_queries(int nq, int Hd) { return nq > 8 && Hd != 256 ? 16 : 8; }
 
 using DecodeFn = void (*)(const KvDecodeArgs);
