@@ -566,8 +566,8 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  *              > max_pages * page_size (that sequence's output is 0),
  *              WSVD_DEVERR_PAGE_RANGE for a bad page (that sequence's output is
  *              not valid).
- * Rows >= seq_lens[b] are never used: their bytes may hold anything.  Two
- * launches.                                                                 */
+ * Rows >= seq_lens[b] are never used: their bytes may hold anything.  One
+ * launch.                                                                   */
 size_t wsvd_latent_append_paged_workspace_size(int B, int T, int E);
 int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int bits, int page_size, int num_pages, int max_pages,
                              int hadamard_block, const void* x, int x_dtype, const void* A_k, const void* A_v,

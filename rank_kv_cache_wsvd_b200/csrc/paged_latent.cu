@@ -19,10 +19,13 @@
 // its cp.async pipeline, its running maximum and sum, its partial results, and
 // where it arrives last at a head, the join and the product with B_Vh.  Nothing
 // waits for a CTA, so one warp's joins are hidden by the others' strips (a
-// ragged int4 batch of 16 x 32 heads: 20.7 us; with the same pipelines joined per
-// CTA 30.0).  Measured, 32 heads: 4 x 32768 rows 33.8 / 50.9 / 89.9 / 172 us for
-// int8 r 16 / 32 / 64 / 128 (4.5 / 5.6 / 6.2 / 6.3 TB/s) and 40.0 / 54.2 / 96.0 for
-// int4 r 32 / 64 / 128; one sequence of 1600 rows 9.0 us.  Bound by HBM from 64-byte
+// ragged int4 batch of 16 x 32 heads: 20.6 us; with the same pipelines joined per
+// CTA 30.0).  A warp projects q' itself at the start of a segment while its first
+// strips arrive: with a q' kernel ahead of this one the ragged batch took 20.6 us
+// against 18.9, long caches 1 to 3 us less, and every call a second launch (2.5 us
+// of host time).  Measured, 32 heads: 4 x 32768 rows 34.5 / 51.9 / 91.5 / 175 us for
+// int8 r 16 / 32 / 64 / 128 (4.4 / 5.5 / 6.1 / 6.2 TB/s) and 42.1 / 56.1 / 100 for
+// int4 r 32 / 64 / 128; one sequence of 1600 rows 9.3 us.  Bound by HBM from 64-byte
 // rows on; shorter rows by the instructions a row costs whatever its length.
 #include <math.h>
 
@@ -67,8 +70,9 @@ struct LatDecodeArgs {
   const int32_t* block_table;
   const uint8_t *lat_k, *lat_v;
   const __half *scale_k, *scale_v;
-  const float* qglobal;  // [B][H][r]
-  const __half* Bv;      // [H][r][Hd]
+  const uint16_t* q;     // [B][H][Hd]
+  int q_dtype;
+  const __half *Bk, *Bv; // [H][r][Hd]
   float* out;
   float* partials;       // [kMaxDecodeCtas + B * H][r + 2]: o, then m, l
   int32_t* counters;
@@ -123,6 +127,63 @@ __device__ __forceinline__ uint32_t bytes_of(const uint4& w, uint32_t sel) {
   return __byte_perm(__byte_perm(w.x, w.y, sel), __byte_perm(w.z, w.w, sel), 0x5410);
 }
 
+// A warp's q' = bk . q, bk [R][Hd] fp16, Hd <= 64 N: eight lanes to a row, four
+// rows at a time.  Returns the lane's largest |q'|.
+template <int R, int N>
+__device__ __forceinline__ float project_query(const uint16_t* q, int dtype, const __half* bk, int Hd, float* out,
+                                               int lane) {
+  const int sub = lane & 7, part = lane >> 3;
+  float x[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int d = (i * 8 + sub) * 8;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (d < Hd) w = __ldg(reinterpret_cast<const uint4*>(q + d));
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = dtype == WSVD_DTYPE_BF16
+                           ? make_float2(__uint_as_float(ws[k] << 16), __uint_as_float(ws[k] & 0xffff0000u))
+                           : h2_pair(ws[k]);
+      x[i][2 * k] = f.x;
+      x[i][2 * k + 1] = f.y;
+    }
+  }
+  float amax = 0.f;
+  constexpr int kFly = R / 4 < 8 ? R / 4 : (N == 4 ? 4 : 8);  // turns whose loads are in flight together
+#pragma unroll 1
+  for (int j0 = 0; j0 < R; j0 += 4 * kFly) {
+    uint4 w[kFly][N];
+#pragma unroll
+    for (int j = 0; j < kFly; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int d = (i * 8 + sub) * 8;
+        w[j][i] = make_uint4(0, 0, 0, 0);
+        if (d < Hd) w[j][i] = __ldg(reinterpret_cast<const uint4*>(bk + (size_t)(j0 + 4 * j + part) * Hd + d));
+      }
+#pragma unroll
+    for (int j = 0; j < kFly; ++j) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t ws[4] = {w[j][i].x, w[j][i].y, w[j][i].z, w[j][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = h2_pair(ws[k]);
+          v = fmaf(f.x, x[i][2 * k], v);
+          v = fmaf(f.y, x[i][2 * k + 1], v);
+        }
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (sub == 0) out[j0 + 4 * j + part] = v;
+      amax = fmaxf(amax, fabsf(v));
+    }
+  }
+  return amax;
+}
+
 // A warp's out[0 .. 32 N) = (o . inv) . bv, bv [R][32 N] fp16; lane i columns N i ..
 template <int R, int N>
 __device__ __forceinline__ void up_project(const float* o, float inv, const __half* bv, float* out, int lane) {
@@ -169,10 +230,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
       for (int i = tid; i < H * Hd; i += C::kThreads) a.out[(size_t)b * H * Hd + i] = 0.f;
   Strips<TS, C::kLead> share;
   typename Strips<TS, C::kLead>::Segment seg;
-  if (!share.deal(seqs, me, min((int)gridDim.x * NW, kMaxDecodeCtas), 1, a.err, &seg)) {
-    griddep_wait();  // the grid never completes before the q' grid it was launched behind
-    return;
-  }
+  if (!share.deal(seqs, me, min((int)gridDim.x * NW, kMaxDecodeCtas), 1, a.err, &seg)) return;
 
   // ---- the warp's copies: cursor `ld`; lane i holds the page of 16-row group i
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
@@ -232,7 +290,6 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
   settle();
   for (int i = 0; i < S - 1; ++i) issue(i);
   int stage = 0;
-  griddep_wait();  // q'
 
   // A lane's row within a block of 32, in the score product's order of rows.
   const int tok = ((c4 >> 1) << 4) | ((c4 & 1) << 3) | g;
@@ -250,14 +307,11 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
     uint32_t qhm[KS][2], qlo[KS][2];
     float qstep;
     {
-      const float* qg = a.qglobal + bh * R;
-      float amax = 0.f;
-#pragma unroll
-      for (int j0 = 0; j0 < R; j0 += 32) {
-        const float v = j0 + lane < R ? __ldcg(qg + j0 + lane) : 0.f;
-        if (j0 + lane < R) sm_q[warp][j0 + lane] = v;
-        amax = fmaxf(amax, fabsf(v));
-      }
+      const uint16_t* q = a.q + bh * Hd;
+      const __half* bk = a.Bk + (size_t)h * R * Hd;
+      float amax = Hd == 128  ? project_query<R, 2>(q, a.q_dtype, bk, Hd, sm_q[warp], lane)
+                   : Hd == 256 ? project_query<R, 4>(q, a.q_dtype, bk, Hd, sm_q[warp], lane)
+                               : project_query<R, 1>(q, a.q_dtype, bk, Hd, sm_q[warp], lane);
       amax = key_float(warp_max_s32(float_key(amax)));
       __syncwarp();
       const float inv = amax > 0.f ? (float)kDigitMax / amax : 0.f;
@@ -595,28 +649,18 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   a.out = out;
   a.partials = reinterpret_cast<float*>(w);
   a.counters = reinterpret_cast<int32_t*>(w + counters);
-  float* qglobal = reinterpret_cast<float*>(w + counters + align16((size_t)B * H * 4));
-  a.qglobal = qglobal;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_dtype = q_dtype;
+  a.Bk = static_cast<const __half*>(B_k);
   a.err = err;
   a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();
   if (paged_resident_ctas(kern.fn, kern.threads, kern.smem, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
-  // q' for every (b, h) first; the decode is launched behind it as its
-  // programmatic dependent and copies its first strips meanwhile.
-  if (launch_qproj(B, H, Hd, r, q, q_dtype, B_k, nullptr, 0, qglobal, s, false) != cudaSuccess) return WSVD_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.ctas);
-  cfg.blockDim = dim3((unsigned)kern.threads);
-  cfg.dynamicSmemBytes = kern.smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   void* args[] = {&a};
-  return cudaLaunchKernelExC(&cfg, kern.fn, args) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+  return cudaLaunchKernel(kern.fn, dim3((unsigned)a.ctas), dim3((unsigned)kern.threads), args, kern.smem, s) == cudaSuccess
+             ? WSVD_OK
+             : WSVD_ERR_CUDA;
 }
 
 extern "C" size_t wsvd_latent_append_paged_workspace_size(int B, int T, int E) {
