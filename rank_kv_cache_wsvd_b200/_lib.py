@@ -315,6 +315,14 @@ def shared_latent_svd_decode(q, lat_k, lat_v, B_k, B_v, seq_lens, softmax_scale:
 # ----------------------------------------------------------------------------- paged dense cache
 # The calls below check all their arguments but are written flat: at the sizes
 # of one decode step a call's host time is what a caller waits for.
+def _device_of(t):
+    """Index of the CUDA device a call's first tensor lies on."""
+    index = t.get_device()
+    if index < 0:
+        raise WsvdError("all tensors must be CUDA tensors")
+    return index
+
+
 def _dense(t, dtype, shape, index, name):
     """Address of a dense tensor on cuda:index with the dtype and shape given."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
@@ -396,7 +404,7 @@ def paged_kv_append(k, v, k_pages, v_pages, block_table, seq_lens, q=None, q_out
     B, T, Hkv, Hd = k.shape
     num_pages, _, page_size, _ = k_pages.shape
     max_pages = block_table.shape[1]
-    dtype, dev, i32 = k.dtype, k.get_device(), torch.int32
+    dtype, dev, i32 = k.dtype, _device_of(k), torch.int32
     code = _dtype_code(k)
     pk, sk = _tokens(k, dtype, (B, T, Hkv, Hd), dev, "k")
     pv, sv = _tokens(v, dtype, (B, T, Hkv, Hd), dev, "v")
@@ -442,7 +450,7 @@ def paged_decode_attention(q, k_pages, v_pages, block_table, seq_lens, softmax_s
         Tq = 1
     num_pages, Hkv, page_size, _ = k_pages.shape
     max_pages = block_table.shape[1]
-    dtype, dev = q.dtype, q.get_device()
+    dtype, dev = q.dtype, _device_of(q)
     code = _dtype_code(q)
     if out is None:
         out = _new(torch.empty, shape, torch.float32, dev, stream)
@@ -475,7 +483,7 @@ def wsvd_latent_append_paged(x, A_k, A_v, seq_lens, block_table, lat_k, lat_v, s
     H, _, r = A_k.shape
     num_pages, _, page_size, rb = lat_k.shape
     max_pages = block_table.shape[1]
-    dev, i32, f16, u8 = x.get_device(), torch.int32, torch.float16, torch.uint8
+    dev, i32, f16, u8 = _device_of(x), torch.int32, torch.float16, torch.uint8
     code = _dtype_code(x)
     codes, scales, downs = (num_pages, H, page_size, r * bits // 8), (num_pages, H, page_size), (H, E, r)
     pl = _dense(seq_lens, i32, (B,), dev, "seq_lens")
@@ -501,7 +509,7 @@ def wsvd_decode_attention_paged(q, lat_k, lat_v, scale_k, scale_v, B_k, B_v, blo
     B, H, Hd = shape = q.shape
     num_pages, _, page_size, rb = lat_k.shape
     max_pages = block_table.shape[1]
-    r, dev, f16, u8 = rb * 8 // bits, q.get_device(), torch.float16, torch.uint8
+    r, dev, f16, u8 = rb * 8 // bits, _device_of(q), torch.float16, torch.uint8
     code = _dtype_code(q)
     if out is None:
         out = _new(torch.empty, shape, torch.float32, dev, stream)

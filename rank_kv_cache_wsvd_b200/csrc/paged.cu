@@ -772,7 +772,7 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
   if (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256) return WSVD_ERR_UNSUPPORTED;
   if (rot_dim % 16) return WSVD_ERR_UNSUPPORTED;
   const int shift = page_shift_of(page_size);
-  if (shift < 0 || B > 65535) return WSVD_ERR_UNSUPPORTED;
+  if (shift < 0 || B > 65535 || (long long)Hq + 2LL * Hkv > (1 << 20)) return WSVD_ERR_UNSUPPORTED;
   if ((long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
   if (!block_table || !seq_lens || !seq_lens_out || !k_pages || !v_pages || !workspace) return WSVD_ERR_INVALID_ARG;
   if (T > 0 && (!k || !v || (Hq > 0 && (!q || !q_out)))) return WSVD_ERR_INVALID_ARG;
@@ -847,7 +847,7 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   if (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256) return WSVD_ERR_UNSUPPORTED;
   const int shift = page_shift_of(page_size);
   const long long nq = (long long)(Hq / Hkv) * Tq;
-  if (shift < 0 || B > 65535 || nq > 64) return WSVD_ERR_UNSUPPORTED;
+  if (shift < 0 || B > 65535 || nq > 64 || (long long)Tq * Hq * Hd > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
   if ((long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
   if (!seq_lens || !block_table || !q || !k_pages || !v_pages || !out || !workspace) return WSVD_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))

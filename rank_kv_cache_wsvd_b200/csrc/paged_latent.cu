@@ -624,7 +624,7 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
   if (r < 1 || (r * bits) % 8) return WSVD_ERR_INVALID_ARG;
   if (q_dtype != WSVD_DTYPE_FP16 && q_dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
-  if (B > 4096 || (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256)) return WSVD_ERR_UNSUPPORTED;
+  if (B > 4096 || H > (1 << 20) || (Hd != 32 && Hd != 64 && Hd != 128 && Hd != 256)) return WSVD_ERR_UNSUPPORTED;
   const int shift = page_shift_of(page_size);
   LatKernel kern;
   if (shift < 0 || !pick_lat(bits, r * bits / 8, &kern)) return WSVD_ERR_UNSUPPORTED;

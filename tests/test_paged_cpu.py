@@ -1,0 +1,236 @@
+"""Host-side checks of the paged cache calls: every refusal comes before any
+CUDA call (so these run without a GPU), the workspaces hold what the header says,
+and the float64 oracle agrees with hand-worked and independent values."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rank_kv_cache_wsvd_b200 as W
+from oracle import paged_oracle as P
+from rank_kv_cache_wsvd_b200 import _lib
+
+MIB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+    if not os.path.exists(_lib.LIB_PATH):
+        from rank_kv_cache_wsvd_b200 import build
+        build.build()
+    return _lib.load()
+
+
+def _at(mib):
+    """A made-up, aligned address; never dereferenced."""
+    return ctypes.c_void_p(mib * MIB)
+
+
+def _append_args(**kw):
+    a = dict(B=2, T=3, Hq=4, Hkv=2, Hd=64, rot=64, inter=0, page=16, pages=8, maxp=4, maxpos=64, k=_at(1), ks=128,
+             v=_at(2), vs=128, q=_at(3), qs=256, dtype=1, cs=_at(4), news=None, table=_at(5), lens=_at(6), out=_at(6),
+             kp=_at(7), vp=_at(8), qo=_at(9), ws=_at(10), wsb=16, err=None, stream=None)
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    return list(a.values())
+
+
+def _decode_args(**kw):
+    a = dict(B=2, Tq=1, Hq=4, Hkv=2, Hd=64, page=16, pages=8, maxp=4, lens=_at(1), table=_at(2), q=_at(3), kp=_at(4),
+             vp=_at(5), dtype=1, scale=0.0, out=_at(6), ws=_at(7), wsb=64 * MIB, err=None, stream=None)
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    return list(a.values())
+
+
+def _lat_decode_args(**kw):
+    a = dict(B=2, H=4, Hd=64, r=32, bits=8, page=16, pages=8, maxp=4, lens=_at(1), table=_at(2), q=_at(3), dtype=1,
+             lk=_at(4), lv=_at(5), sk=_at(6), sv=_at(7), Bk=_at(8), Bv=_at(9), scale=0.0, out=_at(10), ws=_at(11),
+             wsb=64 * MIB, err=None, stream=None)
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    return list(a.values())
+
+
+def _lat_append_args(**kw):
+    a = dict(B=2, T=3, H=4, E=256, r=32, bits=8, page=16, pages=8, maxp=4, blk=128, x=_at(1), dtype=1, Ak=_at(2),
+             Av=_at(3), lens=_at(4), out=_at(4), table=_at(5), lk=_at(6), lv=_at(7), sk=_at(8), sv=_at(9), ws=_at(10),
+             wsb=64 * MIB, err=None, stream=None)
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    return list(a.values())
+
+
+BAD = ctypes.c_void_p(MIB + 8)  # not 16-byte aligned
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), 1), (dict(T=-1), 1), (dict(Hkv=0), 1), (dict(dtype=2), 1), (dict(rot=-16), 1), (dict(rot=80), 1),
+    (dict(Hd=48), 1), (dict(Hd=48, rot=16), 2), (dict(Hd=512), 2), (dict(rot=24), 2), (dict(page=8), 2), (dict(page=48), 2), (dict(page=512), 2),
+    (dict(B=65536), 2), (dict(maxp=1 << 28, page=16), 2), (dict(k=None), 1), (dict(v=None), 1), (dict(q=None), 1),
+    (dict(qo=None), 1), (dict(cs=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(out=None), 1),
+    (dict(kp=None), 1), (dict(ws=None), 1), (dict(k=BAD), 1), (dict(q=BAD), 1), (dict(vp=BAD), 1), (dict(cs=BAD), 1),
+    (dict(ks=120), 1), (dict(vs=132), 1), (dict(qs=248), 1), (dict(wsb=8), 4), (dict(B=0, k=None, table=None), 0),
+    (dict(qo=_at(1)), 1),                                   # q_out over k
+    (dict(qo=_at(3), qs=512), 1),                           # in place over a strided q
+    (dict(kp=_at(3)), 1), (dict(vp=_at(7)), 1),             # pages over q, both pools one
+    (dict(out=ctypes.c_void_p(6 * MIB + 4)), 1),            # lengths shifted by one
+    (dict(out=_at(5)), 1), (dict(news=_at(7)), 1),          # lengths over the table, counts inside a pool
+])
+def test_kv_append_refuses(lib, kw, want):
+    assert lib.paged_kv_append(*_append_args(**kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), 1), (dict(Tq=0), 1), (dict(Hkv=0), 1), (dict(Hq=3), 1), (dict(Hq=1), 1), (dict(dtype=-1), 1),
+    (dict(Hd=96), 2), (dict(page=24), 2), (dict(page=1024), 2), (dict(Tq=33), 2), (dict(B=70000), 2),
+    (dict(lens=None), 1), (dict(table=None), 1), (dict(q=None), 1), (dict(kp=None), 1), (dict(vp=None), 1),
+    (dict(out=None), 1), (dict(ws=None), 1), (dict(q=BAD), 1), (dict(kp=BAD), 1), (dict(out=BAD), 1), (dict(ws=BAD), 1),
+    (dict(wsb=1024), 4), (dict(B=0, q=None), 0),
+])
+def test_kv_decode_refuses(lib, kw, want):
+    assert lib.paged_decode_attention(*_decode_args(**kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), 1), (dict(H=0), 1), (dict(bits=6), 1), (dict(r=0), 1), (dict(r=3, bits=4), 1), (dict(dtype=3), 1),
+    (dict(B=4097), 2), (dict(Hd=48), 2), (dict(page=8), 2), (dict(r=24), 2), (dict(r=16, bits=4), 2), (dict(r=256), 2),
+    (dict(lens=None), 1), (dict(table=None), 1), (dict(lk=None), 1), (dict(sv=None), 1), (dict(Bk=None), 1),
+    (dict(out=None), 1), (dict(lv=BAD), 1), (dict(Bv=BAD), 1), (dict(ws=BAD), 1), (dict(wsb=1024), 4),
+    (dict(B=0, q=None), 0),
+])
+def test_latent_decode_refuses(lib, kw, want):
+    assert lib.wsvd_decode_attention_paged(*_lat_decode_args(**kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(E=0), 1), (dict(bits=5), 1), (dict(dtype=2), 1),
+    (dict(page=8), 2), (dict(blk=96), 1), (dict(blk=2048, E=4096), 1), (dict(E=200, blk=128), 1), (dict(r=24), 2),
+    (dict(E=272, blk=16), 2), (dict(E=32768), 2), (dict(x=None), 1), (dict(Ak=None), 1), (dict(lens=None), 1),
+    (dict(table=None), 1), (dict(sk=None), 1), (dict(ws=None), 1), (dict(x=BAD), 1), (dict(lk=BAD), 1), (dict(ws=BAD), 1),
+    (dict(wsb=256), 4), (dict(out=ctypes.c_void_p(4 * MIB + 4)), 1), (dict(out=_at(5)), 1), (dict(B=0, x=None), 0),
+    (dict(T=1, r=24), 2), (dict(T=1, blk=96), 1), (dict(T=1, B=17, E=272, blk=16), 2), (dict(T=1, x=None), 1),
+])
+def test_latent_append_refuses(lib, kw, want):
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(**kw)) == want
+
+
+def test_workspace_sizes(lib):
+    a16 = lambda v: (v + 15) // 16 * 16
+    assert W.paged_kv_append_workspace_size(1) == 16 and W.paged_kv_append_workspace_size(9) == a16(36)
+    assert W.paged_kv_append_workspace_size(-1) == 0
+    # two partials per CTA of at most 592, of O and (m, l) per query of a chunk; a counter per unit
+    size = lambda B, Hkv, nq, qc, Hd: (a16(2 * 592 * (min(nq, qc) * Hd + (2 * min(nq, qc) + 3) // 4 * 4) * 4)
+                                       + a16(B * Hkv * math.ceil(nq / qc) * 4))
+    assert W.paged_decode_workspace_size(3, 1, 32, 8, 128) == size(3, 8, 4, 8, 128)
+    assert W.paged_decode_workspace_size(3, 4, 32, 4, 64) == size(3, 4, 32, 16, 64)
+    assert W.paged_decode_workspace_size(3, 1, 16, 1, 256) == size(3, 1, 16, 8, 256)
+    assert W.paged_decode_workspace_size(3, 1, 30, 8, 128) == 0
+    assert W.wsvd_latent_append_paged_workspace_size(2, 3, 256) == 256 + W.wsvd_prefill_workspace_size(2, 3, 256)
+
+
+def test_python_refuses_what_it_cannot_pass_on(lib):
+    """Host tensors, wrong types and shapes raise before the library is called."""
+    z = torch.zeros
+    q, kp = z(2, 4, 64, dtype=torch.float16), z(8, 2, 16, 64, dtype=torch.float16)
+    table, lens = z(2, 4, dtype=torch.int32), z(2, dtype=torch.int32)
+    with pytest.raises(W.WsvdError, match="CUDA"):
+        W.paged_decode_attention(q, kp, kp, table, lens)
+    with pytest.raises(W.WsvdError, match="CUDA"):
+        W.paged_kv_append(z(2, 1, 2, 64, dtype=torch.float16), z(2, 1, 2, 64, dtype=torch.float16), kp, kp, table, lens)
+    lat, sc = z(8, 4, 16, 32, dtype=torch.uint8), z(8, 4, 16, dtype=torch.float16)
+    up, down = z(4, 32, 64, dtype=torch.float16), z(4, 256, 32, dtype=torch.float16)
+    with pytest.raises(W.WsvdError, match="CUDA"):
+        W.wsvd_decode_attention_paged(q, lat, lat, sc, sc, up, up, table, lens, 8)
+    with pytest.raises(W.WsvdError, match="CUDA"):
+        W.wsvd_latent_append_paged(z(2, 1, 256, dtype=torch.bfloat16), down, down, lens, table, lat, lat, sc, sc, 8)
+
+
+def test_strided_tokens_are_recognised():
+    """A slice of a fused projection passes with its token stride; transposed
+    heads, uneven batches and broadcast axes are refused."""
+    fused = torch.zeros(3, 5, 10 * 32, dtype=torch.float16)
+    part = fused[..., 64:128].unflatten(-1, (2, 32))
+    ptr, stride = _lib._tokens(part, torch.float16, (3, 5, 2, 32), -1, "k")
+    assert (ptr, stride) == (part.data_ptr(), 320)
+    one = fused[:, 2:3, 64:128].unflatten(-1, (2, 32))   # one token of each sequence: five tokens apart
+    assert _lib._tokens(one, torch.float16, (3, 1, 2, 32), -1, "k")[1] == 1600
+    alone = fused[1:2, 2:3, 64:128].unflatten(-1, (2, 32))
+    assert _lib._tokens(alone, torch.float16, (1, 1, 2, 32), -1, "k")[1] == 64
+    for bad in (part.transpose(0, 1), part[..., ::2], part.transpose(2, 3), fused[:, :4, 64:128].unflatten(-1, (2, 32)),
+                part[:, :1].expand(3, 5, 2, 32)):
+        with pytest.raises(W.WsvdError):
+            _lib._tokens(bad, torch.float16, tuple(bad.shape), -1, "k")
+
+
+# ----------------------------------------------------------------------------- the oracle itself
+def test_oracle_rotation_by_hand_and_as_complex_numbers():
+    quarter = np.array([0.0, 0.0, 1.0, 1.0])  # cos, sin of a quarter turn for both pairs
+    x = np.array([1.0, 2.0, 3.0, 4.0, 9.0])
+    assert np.allclose(P.rotate(x, quarter, 4, False), [-3, -4, 1, 2, 9])
+    assert np.allclose(P.rotate(x, quarter, 4, True), [-2, 1, -4, 3, 9])
+    rng = np.random.default_rng(0)
+    a, x = rng.uniform(0, 6, 8), rng.standard_normal((3, 16))
+    cs = np.concatenate([np.cos(a), np.sin(a)])
+    z = (x[:, :8] + 1j * x[:, 8:]) * np.exp(1j * a)
+    assert np.allclose(P.rotate(x, cs, 16, False), np.concatenate([z.real, z.imag], axis=1))
+    z = (x[:, 0::2] + 1j * x[:, 1::2]) * np.exp(1j * a)
+    assert np.allclose(P.rotate(x, cs, 16, True), np.stack([z.real, z.imag], axis=-1).reshape(3, 16))
+
+
+def test_oracle_decode_against_torch():
+    rng = np.random.default_rng(1)
+    table = np.array([[2, 0], [1, 3]])
+    K, V = rng.standard_normal((4, 2, 16, 8)), rng.standard_normal((4, 2, 16, 8))
+    q, lens = rng.standard_normal((2, 3, 4, 8)), [20, 2]
+    out, mass, _ = P.decode(q, K, V, table, lens)
+    for b, n in enumerate(lens):
+        Kb, Vb = (torch.from_numpy(P.rows(x, table, b, n)) for x in (K, V))
+        for t in range(3):
+            m = n - 2 + t
+            for h in range(4):
+                if m <= 0:
+                    assert (out[b, t, h] == 0).all()
+                    continue
+                p = torch.softmax(Kb[:m, h // 2] @ torch.from_numpy(q[b, t, h]) / math.sqrt(8), 0)
+                assert np.allclose(out[b, t, h], (p @ Vb[:m, h // 2]).numpy())
+    assert (mass >= np.abs(out) - 1e-12).all()
+
+
+def test_oracle_latent_decode_against_the_contiguous_oracle():
+    import oracle as O
+    rng = np.random.default_rng(2)
+    H, r, Hd = 2, 16, 32
+    for bits in (8, 4):
+        lat = [rng.integers(0, 256, (3, H, 16, r * bits // 8), dtype=np.uint8) for _ in range(2)]
+        sc = [(rng.random((3, H, 16)) * 0.1).astype(np.float16) for _ in range(2)]
+        up = [rng.standard_normal((H, r, Hd)).astype(np.float16) for _ in range(2)]
+        table, lens = np.array([[2, 0]]), np.array([21], np.int32)
+        q = rng.standard_normal((1, H, Hd))
+        flat = [np.concatenate([x[2], x[0]], axis=1)[None] for x in lat + sc]
+        want = O.wsvd_decode(q, flat[0], flat[2], flat[1], flat[3], up[0], up[1], lens, r, bits)
+        got, _, _ = P.latent_decode(q, lat[0], lat[1], sc[0], sc[1], up[0], up[1], table, lens, bits)
+        assert np.allclose(got, want, rtol=1e-9, atol=1e-12)
+
+
+def test_an_allowance_catches_planted_mistakes():
+    """The tolerance of the decode tests refuses a row too many, a row too few,
+    a neighbour's page and weights rounded to bf16."""
+    rng = np.random.default_rng(3)
+    table, lens = np.array([[0, 1, 2, 3]]), [50]
+    K, V = rng.standard_normal((5, 1, 16, 64)), rng.standard_normal((5, 1, 16, 64))
+    q = rng.standard_normal((1, 1, 2, 64))
+    ref, mass, wobble = P.decode(q, K, V, table, lens)
+    allow = P.decode_allowance(mass, wobble, 64, 50)
+    off = lambda out: float((np.abs(out - ref) / allow).max())
+    assert off(P.decode(q, K, V, table, [51])[0]) > 1 and off(P.decode(q, K, V, table, [49])[0]) > 1
+    assert off(P.decode(q, K, V, np.array([[0, 1, 4, 3]]), lens)[0]) > 1
+    Kr, Vr = P.rows(K, table, 0, 50)[:, 0], P.rows(V, table, 0, 50)[:, 0]
+    p = np.exp(Kr @ q[0, 0, 0] / 8 - (Kr @ q[0, 0, 0] / 8).max())
+    p16 = torch.from_numpy(p).bfloat16().double().numpy()
+    rounded = ref.copy()
+    rounded[0, 0, 0] = p16 @ Vr / p.sum()
+    assert off(rounded) > 1

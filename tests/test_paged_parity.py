@@ -383,6 +383,50 @@ def test_append_and_decode_as_used():
         _check_decode(out, qo, kp.nan_to_num(0), vp.nan_to_num(0), table, lens, what=f"replay {i}")
 
 
+def test_calls_refuse_wrong_tensors():
+    """Types, shapes and layouts that do not fit raise before a launch; tensors of
+    another device too."""
+    lens = [20, 9]
+    kp, vp, table = _cache(lens, 2, 64, 16, "fp16", seed=1)
+    q, tab, n = randn((2, 4, 64), "fp16", 2), cuda(table), cuda(np.asarray(lens, np.int32))
+    out = torch.empty((2, 4, 64), device="cuda")
+    call = lambda **kw: W.paged_decode_attention(**{**dict(q=q, k_pages=kp, v_pages=vp, block_table=tab, seq_lens=n), **kw})
+    for kw in (dict(q=q.float()), dict(q=q.bfloat16()), dict(k_pages=kp[:, :1]), dict(v_pages=vp.transpose(1, 2)),
+               dict(v_pages=vp[:-1]), dict(block_table=tab.long()), dict(block_table=tab[:1]), dict(seq_lens=n[:1]),
+               dict(seq_lens=n.long()), dict(out=out[:, :2]), dict(out=out.half()), dict(q=q.cpu()), dict(seq_lens=n.cpu()),
+               dict(q=torch.cat([q, q], 2)[..., ::2]), dict(workspace_buf=torch.zeros(4, device="cuda")),
+               dict(workspace_buf=W.workspace(64)), dict(softmax_scale=0.0, err=torch.zeros(1, device="cuda"))):
+        with pytest.raises(W.WsvdError):
+            call(**kw)
+    with pytest.raises(W.WsvdError):  # three query heads over two
+        call(q=q[:, :3].contiguous())
+    k = randn((2, 1, 2, 64), "fp16", 3)
+    put = lambda **kw: W.paged_kv_append(**{**dict(k=k, v=k, k_pages=kp, v_pages=vp, block_table=tab, seq_lens=n), **kw})
+    before = n.clone(), kp.clone()
+    for kw in (dict(v=k[:, :, :1]), dict(v=k.bfloat16()), dict(q=q[:, None].float()), dict(q_out=q[:, None]),
+               dict(cos_sin=rope_table(64, 64).half()), dict(cos_sin=rope_table(64, 24)), dict(new_lens=n.long()),
+               dict(seq_lens_out=n[:1]), dict(k_pages=kp.float()), dict(q=q[:, None], q_out=kp.view(-1)[:512].view(2, 1, 4, 64))):
+        with pytest.raises(W.WsvdError):
+            put(**kw)
+    torch.cuda.synchronize()
+    assert torch.equal(n, before[0]) and torch.equal(kp.view(torch.int16), before[1].view(torch.int16))
+    out = call()
+    assert torch.isfinite(out).all()
+
+
+def test_decode_thousands_of_short_sequences():
+    B, Hkv = 4500, 1
+    lens = [(b * 5) % 23 for b in range(B)]
+    kp, vp, table = _cache(lens, Hkv, 32, 16, "fp16", seed=3)
+    q = randn((B, 1, 2, 32), "fp16", 4)
+    out, err = _decode(q, kp, vp, table, lens)
+    assert err == 0
+    some = list(range(0, 60)) + list(range(B - 60, B))
+    _check_decode(out[some], q[some], kp.nan_to_num(0), vp.nan_to_num(0), table[some], [lens[b] for b in some], what="many")
+    assert (out[[b for b in range(B) if lens[b] == 0]] == 0).all()
+    assert torch.isfinite(out).all()
+
+
 def test_paged_decode_matches_the_contiguous_one():
     """The same rows in pages and in the dense cache: both within the allowance
     of the float64 value."""
