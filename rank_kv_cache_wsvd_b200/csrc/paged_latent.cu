@@ -585,31 +585,8 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 constexpr size_t kPagedCounterBytes = 256;
 
 // Sequences up to which one token each takes the append's GEMV (fp32 FMAs, up to
-// four tokens per pass over the weights) rather than the GEMM.  Measured with
-// 32 heads, E 4096, GEMV / GEMM in us: r 32, 1 / 4 / 8 / 16 sequences 6.8 / 12.3 /
-// 26.7 / 78.3 against 17.7 / 17.9 / 18.5 / 18.7; r 64 9.2 / 22.4 / 40.7 against
-// 23.0 / 25.9 / 20.8; 8 heads of r 32 5.3 / 7.8 / 13.5 / 39.8 against 13.7 / 13.8 /
-// 14.1 / 14.6.
+// four tokens per pass over the weights) rather than the tensor-core GEMM.
 constexpr int kGemvTokens = 4;
-
-// Whether one token of each sequence can take the append's GEMV (the shapes
-// wsvd_latent_append takes), and its arguments.
-bool one_token_append(int B, int H, int E, int r, int bits, int cap, int hadamard_block, const void* x, int x_dtype,
-                      const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k, uint8_t* lat_v,
-                      void* scale_k, void* scale_v, void* counter, int32_t* err, AppendArgs* a) {
-  if (B > 16 || E > 65536 || (r != 8 && r != 16 && r != 32 && r != 64 && r != 128)) return false;
-  if (hadamard_block < 1 || hadamard_block > 1024 || (hadamard_block & (hadamard_block - 1)) || E % hadamard_block)
-    return false;
-  const int cl = append_cluster_size(E, hadamard_block);
-  if (cl < 1 || append_smem_bytes(B, E, r, cl) > 200 * 1024) return false;
-  a->B = B; a->H = H; a->E = E; a->r = r; a->bits = bits; a->L_cap = cap; a->blk = hadamard_block; a->cluster = cl;
-  a->hnorm = (float)(1.0 / sqrt((double)hadamard_block));
-  a->x = x; a->x_dtype = x_dtype; a->Ak = A_k; a->Av = A_v;
-  a->seq_lens = seq_lens; a->lat_k = lat_k; a->lat_v = lat_v;
-  a->scale_k = static_cast<__half*>(scale_k); a->scale_v = static_cast<__half*>(scale_v);
-  a->counter = static_cast<int32_t*>(counter); a->err = err;
-  return true;
-}
 
 }  // namespace
 
@@ -664,7 +641,7 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
 }
 
 extern "C" size_t wsvd_latent_append_paged_workspace_size(int B, int T, int E) {
-  return kPagedCounterBytes + wsvd_prefill_workspace_size(B, T, E);
+  return kPagedCounterBytes + (B < 1 || T < 1 || E < 1 ? 0 : paged_block_scratch(B, T, E));
 }
 
 extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int bits, int page_size, int num_pages,
@@ -675,40 +652,50 @@ extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int b
                                         void* stream) {
   if (B < 0 || T < 0 || H < 1 || E < 1 || r < 1 || num_pages < 0 || max_pages < 0) return WSVD_ERR_INVALID_ARG;
   if (B == 0) return WSVD_OK;
+  if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
+  if (x_dtype != WSVD_DTYPE_FP16 && x_dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
+  if (hadamard_block < 1 || hadamard_block > 1024 || (hadamard_block & (hadamard_block - 1)) || E % hadamard_block)
+    return WSVD_ERR_INVALID_ARG;
   const int shift = page_shift_of(page_size);
-  if (shift < 0 || (long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
+  LatKernel reader;  // rows that the paged decode can read
+  if (shift < 0 || (r * bits) % 8 || !pick_lat(bits, r * bits / 8, &reader)) return WSVD_ERR_UNSUPPORTED;
+  if ((long long)max_pages << shift > 0x7fffffffLL) return WSVD_ERR_UNSUPPORTED;
   if (!seq_lens || !seq_lens_out || !block_table || !workspace) return WSVD_ERR_INVALID_ARG;
-  if (!aligned16(workspace)) return WSVD_ERR_INVALID_ARG;
+  if (T > 0 && (!x || !A_k || !A_v || !lat_k || !lat_v || !scale_k || !scale_v)) return WSVD_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(A_k) || !aligned16(A_v) || !aligned16(lat_k) || !aligned16(lat_v) ||
+      !aligned16(scale_k) || !aligned16(scale_v) || !aligned16(workspace))
+    return WSVD_ERR_INVALID_ARG;
   if (seq_lens_out != seq_lens && overlap(seq_lens_out, (size_t)B * 4, seq_lens, (size_t)B * 4))
     return WSVD_ERR_INVALID_ARG;
   if (overlap(seq_lens_out, (size_t)B * 4, block_table, (size_t)B * max_pages * 4)) return WSVD_ERR_INVALID_ARG;
+  const int ranks = append_cluster_size(E, hadamard_block);
+  const bool gemm = paged_block_takes(B, T, H, E, r);
+  const bool gemv = T == 1 && B <= 16 && E <= 65536 && ranks > 0 && append_smem_bytes(B, E, r, ranks) <= 200 * 1024;
+  if (T > 0 && !gemm && !gemv) return WSVD_ERR_UNSUPPORTED;
   if (workspace_bytes < wsvd_latent_append_paged_workspace_size(B, T, E)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
-  const int cap = max_pages << shift;
-  const PagedRows place{block_table, max_pages, shift, num_pages, seq_lens_out};
-  int32_t* lens = const_cast<int32_t*>(seq_lens);  // read only: PagedRows writes seq_lens_out
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) {
     if (seq_lens_out != seq_lens &&
-        cudaMemcpyAsync(seq_lens_out, seq_lens, (size_t)B * 4, cudaMemcpyDeviceToDevice,
-                        reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        cudaMemcpyAsync(seq_lens_out, seq_lens, (size_t)B * 4, cudaMemcpyDeviceToDevice, s) != cudaSuccess)
       return WSVD_ERR_CUDA;
     return WSVD_OK;
   }
-  if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
-  if (x_dtype != WSVD_DTYPE_FP16 && x_dtype != WSVD_DTYPE_BF16) return WSVD_ERR_INVALID_ARG;
-  if (!x || !A_k || !A_v || !lat_k || !lat_v || !scale_k || !scale_v) return WSVD_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(A_k) || !aligned16(A_v) || !aligned16(lat_k) || !aligned16(lat_v) ||
-      !aligned16(scale_k) || !aligned16(scale_v))
-    return WSVD_ERR_INVALID_ARG;
-  // One token of few sequences, and of up to 16 where E does not suit the GEMM:
-  // the append's GEMV, bound by reading A once; all else the prefill's GEMM.
+  const PagedRows place{block_table, max_pages, shift, num_pages, seq_lens_out};
   AppendArgs a{};
-  const bool gemm = E % 64 == 0 && E <= 16384;
-  if (T == 1 && (B <= kGemvTokens || !gemm) && one_token_append(B, H, E, r, bits, cap, hadamard_block, x, x_dtype, A_k, A_v, lens, lat_k, lat_v,
-                                 scale_k, scale_v, workspace, err, &a)) {
-    (void)cudaGetLastError();
-    return launch_append_paged(a, place, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
-  }
-  return prefill_paged(place, B, T, H, E, r, bits, cap, hadamard_block, x, x_dtype, A_k, A_v, lens, lat_k, lat_v, scale_k,
-                    scale_v, static_cast<uint8_t*>(workspace) + kPagedCounterBytes, workspace_bytes - kPagedCounterBytes,
-                    err, stream);
+  a.B = B; a.H = H; a.E = E; a.r = r; a.bits = bits; a.L_cap = max_pages << shift; a.blk = hadamard_block;
+  a.cluster = ranks;
+  a.hnorm = (float)(1.0 / sqrt((double)hadamard_block));
+  a.x = x; a.x_dtype = x_dtype; a.Ak = A_k; a.Av = A_v;
+  a.seq_lens = const_cast<int32_t*>(seq_lens);  // read only: PagedRows writes seq_lens_out
+  a.lat_k = lat_k; a.lat_v = lat_v;
+  a.scale_k = static_cast<__half*>(scale_k); a.scale_v = static_cast<__half*>(scale_v);
+  a.counter = static_cast<int32_t*>(workspace); a.err = err;
+  (void)cudaGetLastError();
+  // One token of few sequences, and of up to 16 where E does not suit the GEMM:
+  // the append's GEMV, bound by reading A once; all else the tensor-core GEMM.
+  const cudaError_t e = gemv && (B <= kGemvTokens || !gemm)
+                            ? launch_append_paged(a, place, s)
+                            : launch_paged_block(a, T, place, static_cast<uint8_t*>(workspace) + kPagedCounterBytes, s);
+  return e == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
 }

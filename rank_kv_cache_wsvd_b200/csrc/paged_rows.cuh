@@ -1,5 +1,5 @@
-// Where the latent append and prefill put their rows: the contiguous cache
-// [B][H][L_cap], or pages of a pool.
+// Where an append puts its rows: the contiguous cache [B][H][L_cap], or pages of
+// a pool.
 #pragma once
 
 #include "common.cuh"
@@ -8,7 +8,6 @@
 namespace wsvd {
 
 struct ContiguousRows {
-  static constexpr bool kSplits = false;  // the prefill's tiles are never split over E: its rows keep their bits
   // 0, or the WSVD_DEVERR_* bit for which rows pos .. pos + n - 1 of sequence b are refused.
   __device__ __forceinline__ int refused(int, int pos, int n, int L_cap) const {
     return pos >= 0 && (long long)pos + n <= L_cap ? 0 : WSVD_DEVERR_CACHE_FULL;
@@ -25,7 +24,6 @@ struct ContiguousRows {
 
 // L_cap is the page table's capacity max_pages << page_shift.
 struct PagedRows {
-  static constexpr bool kSplits = true;
   const int32_t* block_table;  // [B][max_pages]
   int max_pages, page_shift, num_pages;
   int32_t* seq_lens_out;       // receives every length
@@ -50,10 +48,11 @@ struct PagedRows {
 // The append of launch_append into pages (fp16 weights); a.L_cap is the page
 // table's capacity.
 cudaError_t launch_append_paged(const AppendArgs& a, const PagedRows& place, cudaStream_t stream);
-// wsvd_latent_prefill's checks and launches for rows in pages (a wsvd_status).
-int prefill_paged(const PagedRows& place, int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
-                  const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k,
-                  uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace, size_t workspace_bytes, int32_t* err,
-                  void* stream);
+// A block of T tokens per sequence into pages (paged_prefill.cu): whether it
+// takes these sizes, its scratch, and its launches (a.L_cap as above, a.counter
+// zero and left zero).
+bool paged_block_takes(int B, int T, int H, int E, int r);
+size_t paged_block_scratch(int B, int T, int E);
+cudaError_t launch_paged_block(const AppendArgs& a, int T, const PagedRows& place, void* scratch, cudaStream_t stream);
 
 }  // namespace wsvd

@@ -29,18 +29,11 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cooperative_groups.h>
-
 #include <algorithm>
-#include <map>
 #include <mutex>
-#include <tuple>
 
 #include "common.cuh"
-#include "paged_rows.cuh"
 #include "tc05.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace wsvd {
 
@@ -336,9 +329,7 @@ __device__ __forceinline__ void load_stage(const PrefillArgs& a, const CopyPlan&
   for (int i = 0; i < kWPieces; ++i) cp_async16_zfill(st + p.w_dst[i], p.w[i] + (size_t)k0 * a.r, p.w_ok[i]);
 }
 
-// PL: where the rows lie (ContiguousRows or PagedRows).
-template <class PL>
-__global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const PrefillArgs a, const PL place) {
+__global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const PrefillArgs a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __half* sm = reinterpret_cast<__half*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -451,7 +442,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const Pre
     if (m >= a.M || n >= a.N) continue;  // warp-uniform
     const int b = m / a.T, t = m - b * a.T;
     const int pos = a.seq_lens[b];
-    if (place.refused(b, pos, a.T, a.L_cap)) continue;  // refused block (flagged by the advance kernel)
+    if (pos < 0 || (long long)pos + a.T > a.L_cap) continue;  // refused block (flagged by the advance kernel)
     const int kv = n / HR, h = (n - kv * HR) / a.r;
     const float ip = a.inv_p[m];
     float cv[4];
@@ -466,7 +457,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const Pre
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
     const float sc = __half2float(sh);
-    const size_t row = place.row(b, h, a.H, pos + t, a.L_cap);
+    const size_t row = ((size_t)b * a.H + h) * a.L_cap + pos + t;
     uint8_t* dst = (kv ? a.lat_v : a.lat_k) + row * RB;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -506,12 +497,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const Pre
 // Numerics are those of the mma.sync kernel above: each k-tile of the hi half
 // is summed from zero on the tensor cores, k-tiles are added with rounding to
 // nearest, the lo half keeps one tensor-core sum.
-//
-// Rows in pages: with few output tiles (small blocks, a batch's new tokens) a
-// cluster of up to 8 CTAs splits E for one tile, each rank walking its own
-// k-tiles; the ranks' sums are read through the cluster's shared memory and
-// added in rank order, each rank quantising its share of the rows.  One CTA's
-// walk over E = 4096 takes 37 us whatever the number of tokens.
 constexpr int kTcBM = 128, kTcBK = 64, kTcStages = 4, kTcThreads = 192;
 
 template <int R, int BN_>
@@ -528,15 +513,12 @@ struct TcCfg {
   static_assert(BN == 64 || BN == 128, "tile width");
   static_assert(R <= BN, "whole heads per tile");
   static constexpr int TCOLS = 512;
-  static constexpr int PITCH = BN + 4;  // floats per row of a split tile's sums
-  static_assert((kTcBM + kTcBM / 2) * PITCH * 4 <= kTcStages * STAGE, "the sums of a split tile fit the ring");
   static constexpr int SMEM = kTcStages * STAGE + 1024 + 256;
   static_assert(STAGE % 1024 == 0, "stages keep the 1024-byte swizzle-atom alignment");
 };
 
 struct TcArgs {
   int M, T, H, bits, L_cap, KT;
-  int ranks;  // CTAs that split E for one tile (rows in pages)
   const float* inv_p;
   const int32_t* seq_lens;
   uint8_t* lat_k;
@@ -566,86 +548,11 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
       : "memory");
 }
-// The rows of a tile whose E a cluster has split (all threads; every rank has
-// left its sums at the start of its ring, scaled back): rank q joins and
-// quantises its share of the rows.
-template <int R, int BN, class PL>
-__device__ __forceinline__ void split_epilogue(const TcArgs& a, const PL& place, uint8_t* smem, int rank, int ranks,
-                                               int m0, int nl, int kv) {
-  using C = TcCfg<R, BN>;
-  constexpr int HEADS = BN / R;
-  cg::cluster_group cluster = cg::this_cluster();
-  float* part = reinterpret_cast<float*>(smem);
-  float* sums = part + kTcBM * C::PITCH;  // [rows of this rank][PITCH]
-  const int r0 = kTcBM * rank / ranks, rows = kTcBM * (rank + 1) / ranks - r0;
-  const int tid = threadIdx.x;
-  cluster.sync();
-  for (int i = tid; i < rows * (BN / 4); i += kTcThreads) {
-    const int row = i / (BN / 4), c = i % (BN / 4) * 4;
-    if (m0 + r0 + row >= a.M) break;
-    float4 x[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < ranks)
-        x[q] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part, q) + (size_t)(r0 + row) * C::PITCH + c);
-    float4 v = x[0];
-#pragma unroll
-    for (int q = 1; q < 8; ++q)
-      if (q < ranks) v = make_float4(v.x + x[q].x, v.y + x[q].y, v.z + x[q].z, v.w + x[q].w);
-    *reinterpret_cast<float4*>(sums + (size_t)row * C::PITCH + c) = v;
-  }
-  cluster.sync();  // the ranks' sums have been read: a rank may leave
-  // LPU threads to a (row, head) unit, COLS of its columns each.
-  constexpr int LPU = R > 32 ? R / 32 : 1, COLS = R / LPU;
-  const int Q = a.bits == 8 ? 127 : 7, RB = R * a.bits / 8;
-  const int units = rows * HEADS * LPU;
-  for (int u = tid; u < (units + 31) / 32 * 32; u += kTcThreads) {  // whole warps: the maximum crosses lanes
-    const int row = u / (HEADS * LPU), hh = u / LPU % HEADS, sub = u % LPU, m = m0 + r0 + row;
-    const bool real = u < units && m < a.M;
-    const float4* src = reinterpret_cast<const float4*>(sums + (size_t)(real ? row : 0) * C::PITCH + hh * R + sub * COLS);
-    float v[COLS], amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < COLS / 4; ++c) {
-      const float4 x = src[c];
-      v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
-      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
-    }
-#pragma unroll
-    for (int o = LPU / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (!real) continue;
-    const int b = m / a.T, t = m - b * a.T, pos = a.seq_lens[b];
-    if (place.refused(b, pos, a.T, a.L_cap)) continue;  // flagged by the advance kernel
-    const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
-    const float sc = __half2float(sh);
-    const size_t crow = place.row(b, nl / R + hh, a.H, pos + t, a.L_cap);
-    auto code = [&](int j) { return sc > 0.f ? max(-Q, min(Q, __float2int_rn(__fdiv_rn(v[j], sc)))) : 0; };
-    uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.lat_v : a.lat_k) + crow * RB + sub * (COLS * a.bits / 8));
-    if (a.bits == 8) {
-#pragma unroll
-      for (int w = 0; w < COLS / 4; ++w) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x |= ((uint32_t)code(4 * w + k) & 0xFFu) << (8 * k);
-        dst[w] = x;
-      }
-    } else {
-#pragma unroll
-      for (int w = 0; w < COLS / 8; ++w) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x |= ((uint32_t)code(8 * w + k) & 0xFu) << (4 * k);
-        dst[w] = x;
-      }
-    }
-    if (sub == 0) (kv ? a.scale_v : a.scale_k)[crow] = sh;
-  }
-}
-
-template <int R, int BN_, class PL>
+template <int R, int BN_>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_xhi, const __grid_constant__ CUtensorMap tm_xlo,
                       const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
-                      const TcArgs a, const PL place) {
+                      const TcArgs a) {
   using C = TcCfg<R, BN_>;
   constexpr int BN = C::BN, NG = C::NG, S = kTcStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -662,8 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   griddep_launch_dependents();  // the length advance behind may launch (it waits for this grid)
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int ranks = PL::kSplits ? a.ranks : 1, rank = (int)blockIdx.x % ranks;  // of the cluster
-  const int m0 = (int)blockIdx.x / ranks * kTcBM, n0 = blockIdx.y * BN;
+  const int m0 = blockIdx.x * kTcBM, n0 = blockIdx.y * BN;
   const int HR = a.H * R;
   const int kv = n0 >= HR ? 1 : 0, nl = n0 - kv * HR;  // tile columns within the K or the V side
   if (tid == 0) {
@@ -691,7 +597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       timed_out = true;
     }
   };
-  const int kt0 = a.KT * rank / ranks, KT = a.KT * (rank + 1) / ranks - kt0;  // this rank's k-tiles
+  const int KT = a.KT;
 
   // The producer and MMA warps run their loops converged (every lane waits,
   // one elected lane issues), so that the copies and MMAs issue at full rate.
@@ -704,12 +610,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       const uint32_t st = base + (uint32_t)(s * C::STAGE);
       mbar_arrive_expect_tx_warp(&full[s], C::STAGE);
-      tma_load_2d_warp(st, &tm_xhi, (kt0 + kt) * kTcBK, m0, &full[s]);
-      tma_load_2d_warp(st + C::A_BYTES, &tm_xlo, (kt0 + kt) * kTcBK, m0, &full[s]);
+      tma_load_2d_warp(st, &tm_xhi, kt * kTcBK, m0, &full[s]);
+      tma_load_2d_warp(st + C::A_BYTES, &tm_xlo, kt * kTcBK, m0, &full[s]);
 #pragma unroll
       for (int g = 0; g < BN / NG; ++g) {
         const int col = nl + g * NG;
-        tma_load_3d_warp(st + 2 * C::A_BYTES + g * (kTcBK * NG * 2), wmap, col % R, (kt0 + kt) * kTcBK, col / R, &full[s]);
+        tma_load_3d_warp(st + 2 * C::A_BYTES + g * (kTcBK * NG * 2), wmap, col % R, kt * kTcBK, col / R, &full[s]);
       }
     }
     for (int kt = std::max(0, KT - S); kt < KT; ++kt) wait(&full[kt % S], (uint32_t)((kt / S) & 1));
@@ -776,16 +682,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc05::fence_before_sync();
     const int m = m0 + row;
-    if (ranks > 1) {  // this rank's sums, over the ring (every copy and MMA has completed)
-      const float ip = m < a.M ? a.inv_p[m] : 0.f;
-      float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + (size_t)row * C::PITCH);
-#pragma unroll
-      for (int c = 0; c < BN; c += 4)
-        dst[c / 4] = make_float4(tot[c] * ip, tot[c + 1] * ip, tot[c + 2] * ip, tot[c + 3] * ip);
-    } else if (m < a.M) {
+    if (m < a.M) {
       const int b = m / a.T, t = m - b * a.T;
       const int pos = a.seq_lens[b];
-      if (!place.refused(b, pos, a.T, a.L_cap)) {  // else flagged by the advance kernel
+      if (pos >= 0 && (long long)pos + a.T <= a.L_cap) {  // else refused (flagged by the advance kernel)
         const float ip = a.inv_p[m];
         const int Q = a.bits == 8 ? 127 : 7;
         constexpr int HEADS = BN / R < 1 ? 1 : BN / R;
@@ -800,7 +700,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
           const float sc = __half2float(sh);
-          const size_t crow = place.row(b, h, a.H, pos + t, a.L_cap);
+          const size_t crow = ((size_t)b * a.H + h) * a.L_cap + pos + t;
           if (a.bits == 8) {
             uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.lat_v : a.lat_k) + crow * R);
 #pragma unroll
@@ -830,9 +730,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-  }
-  if constexpr (PL::kSplits) {
-    if (ranks > 1) split_epilogue<R, BN>(a, place, smem, rank, ranks, m0, nl, kv);
   }
   tc05::fence_before_sync();
   __syncthreads();
@@ -888,109 +785,76 @@ bool encode_weight_map(CUtensorMap* tm, const void* base, int H, int E, int r, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of c CTAs of a tcgen05 kernel that the current device runs at once
-// (asked once per device, kernel and size; 0 on failure).
-template <class K>
-int resident_clusters(K kern, size_t smem, int c) {
-  static std::mutex mu;
-  static std::map<std::tuple<int, const void*, int>, int> known;
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_tuple(dev, reinterpret_cast<const void*>(kern), c);
-  auto it = known.find(key);
-  if (it != known.end()) return it->second;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)c);
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    n = 0;
-  }
-  return known[key] = n;
-}
-
-template <int R, int BN, class PL>
-cudaError_t launch_tc(const PrefillArgs& pa, const PL& place, const void* A_k, const void* A_v, int32_t* err,
-                      cudaStream_t s) {
+template <int R, int BN>
+cudaError_t launch_tc(const PrefillArgs& pa, const void* A_k, const void* A_v, int32_t* err, cudaStream_t s) {
   using C = TcCfg<R, BN>;
   CUtensorMap mh, ml, mk, mv;
   if (!encode_act_map(&mh, pa.xhi, pa.M, pa.E) || !encode_act_map(&ml, pa.xlo, pa.M, pa.E) ||
       !encode_weight_map(&mk, A_k, pa.H, pa.E, R, C::NG) || !encode_weight_map(&mv, A_v, pa.H, pa.E, R, C::NG))
     return cudaErrorInvalidValue;
   cudaError_t e =
-      cudaFuncSetAttribute(prefill_tc_kernel<R, BN, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      cudaFuncSetAttribute(prefill_tc_kernel<R, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   TcArgs ta{};
   ta.M = pa.M; ta.T = pa.T; ta.H = pa.H; ta.bits = pa.bits; ta.L_cap = pa.L_cap; ta.KT = pa.E / kTcBK;
   ta.inv_p = pa.inv_p; ta.seq_lens = pa.seq_lens;
   ta.lat_k = pa.lat_k; ta.lat_v = pa.lat_v; ta.scale_k = pa.scale_k; ta.scale_v = pa.scale_v; ta.err = err;
-  const int tiles = (pa.M + kTcBM - 1) / kTcBM * (pa.N / C::BN);
-  ta.ranks = 1;
-  if (PL::kSplits)  // the most ranks whose clusters all run at once, at least two k-tiles each
-    for (int c = 8; c > 1 && ta.ranks == 1; c >>= 1)
-      if (2 * c <= ta.KT && tiles <= resident_clusters(prefill_tc_kernel<R, BN, PL>, C::SMEM, c)) ta.ranks = c;
-  const dim3 grid((unsigned)((pa.M + kTcBM - 1) / kTcBM * ta.ranks), (unsigned)(pa.N / C::BN));
+  const dim3 grid((unsigned)((pa.M + kTcBM - 1) / kTcBM), (unsigned)(pa.N / C::BN));
   (void)cudaGetLastError();
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)ta.ranks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = ta.ranks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<R, BN, PL>, mh, ml, mk, mv, ta, place);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<R, BN>, mh, ml, mk, mv, ta);
 }
 
 // Output tile width of the tcgen05 path: 128 columns when the tiles hold whole
 // heads of one side and there are enough of them to fill the device (every
 // tile re-reads the activation rows of its m-tile from L2, so wider tiles
-// halve that traffic), or when E may be split over CTAs instead; otherwise 64
-// (r <= 64), or 0 when the path does not apply.
-int tc_tile_width(long long M, int H, int r, bool splits) {
+// halve that traffic); otherwise 64 (r <= 64), or 0 when the path does not
+// apply.
+int tc_tile_width(long long M, int H, int r) {
   if (r != 16 && r != 32 && r != 64 && r != 128) return 0;
   const long long hr = (long long)H * r, mt = (M + kTcBM - 1) / kTcBM;
-  if (hr % 128 == 0 && (r == 128 || splits || mt * (2 * hr / 128) >= 64)) return 128;
+  if (hr % 128 == 0 && (r == 128 || mt * (2 * hr / 128) >= 64)) return 128;
   if (r <= 64 && hr % 64 == 0) return 64;
   return 0;
 }
 
 // ------------------------------------------------------------------ 3. lengths
-template <class PL>
-__global__ void prefill_advance_kernel(int32_t* seq_lens, int B, int T, int L_cap, const PL place, int32_t* err) {
+__global__ void prefill_advance_kernel(int32_t* seq_lens, int B, int T, int L_cap, int32_t* err) {
   griddep_wait();  // launched as a programmatic dependent of the GEMM, which reads the lengths
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
     const int pos = seq_lens[b];
-    const int why = place.refused(b, pos, T, L_cap);
-    place.advance(seq_lens, b, pos, T, why == 0);
-    if (why) set_err(err, why);
+    if (pos >= 0 && (long long)pos + T <= L_cap) seq_lens[b] = pos + T;
+    else set_err(err, WSVD_DEVERR_CACHE_FULL);
   }
 }
 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// wsvd_latent_prefill's checks and launches for rows that lie as `place` says.
-template <class PL>
-int prefill_at(const PL& place, int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
-               const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k,
-               uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace, size_t workspace_bytes, int32_t* err,
-               void* stream) {
+}  // namespace
+
+}  // namespace wsvd
+
+extern "C" size_t wsvd_prefill_workspace_size(int B, int T, int E) {
+  if (B < 1 || T < 1 || E < 1) return 0;
+  const size_t M = (size_t)B * T;
+  return 2 * wsvd::align16(M * E * 2) + wsvd::align16(M * 4);
+}
+
+extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
+                                   const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens,
+                                   uint8_t* lat_k, uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace,
+                                   size_t workspace_bytes, int32_t* err, void* stream) {
+  using namespace wsvd;
   if (B < 0 || T < 0 || H < 1 || E < 1 || r < 1 || L_cap < 0) return WSVD_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return WSVD_OK;
   if (bits != 8 && bits != 4) return WSVD_ERR_INVALID_ARG;
@@ -1026,7 +890,7 @@ int prefill_at(const PL& place, int B, int T, int H, int E, int r, int bits, int
   const size_t rot_smem = (size_t)E * 4;
   if (cudaFuncSetAttribute(prefill_rotate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rot_smem) !=
           cudaSuccess ||
-      cudaFuncSetAttribute(prefill_gemm_kernel<PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem) !=
+      cudaFuncSetAttribute(prefill_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem) !=
           cudaSuccess)
     return WSVD_ERR_CUDA;
   const float hnorm = (float)(1.0 / sqrt((double)hadamard_block));
@@ -1056,27 +920,27 @@ int prefill_at(const PL& place, int B, int T, int H, int E, int r, int bits, int
     prefill_rotate_kernel<<<(unsigned)M, kRotThreads, rot_smem, s>>>(x, x_dtype, E, hadamard_block, hnorm, whi, wlo,
                                                                      winv);
   }
-  const int bn = tc_tile_width(M, H, r, PL::kSplits);
+  const int bn = tc_tile_width(M, H, r);
   if (bn) {
     cudaError_t e = cudaSuccess;
     if (bn == 128) {
       switch (r) {
-        case 16: e = launch_tc<16, 128>(a, place, A_k, A_v, err, s); break;
-        case 32: e = launch_tc<32, 128>(a, place, A_k, A_v, err, s); break;
-        case 64: e = launch_tc<64, 128>(a, place, A_k, A_v, err, s); break;
-        default: e = launch_tc<128, 128>(a, place, A_k, A_v, err, s); break;
+        case 16: e = launch_tc<16, 128>(a, A_k, A_v, err, s); break;
+        case 32: e = launch_tc<32, 128>(a, A_k, A_v, err, s); break;
+        case 64: e = launch_tc<64, 128>(a, A_k, A_v, err, s); break;
+        default: e = launch_tc<128, 128>(a, A_k, A_v, err, s); break;
       }
     } else {
       switch (r) {
-        case 16: e = launch_tc<16, 64>(a, place, A_k, A_v, err, s); break;
-        case 32: e = launch_tc<32, 64>(a, place, A_k, A_v, err, s); break;
-        default: e = launch_tc<64, 64>(a, place, A_k, A_v, err, s); break;
+        case 16: e = launch_tc<16, 64>(a, A_k, A_v, err, s); break;
+        case 32: e = launch_tc<32, 64>(a, A_k, A_v, err, s); break;
+        default: e = launch_tc<64, 64>(a, A_k, A_v, err, s); break;
       }
     }
     if (e != cudaSuccess) return WSVD_ERR_CUDA;
   } else {
     const dim3 grid((unsigned)((M + kBM - 1) / kBM), (unsigned)((N + kBN - 1) / kBN));
-    prefill_gemm_kernel<PL><<<grid, kGemmThreads, kGemmSmem, s>>>(a, place);
+    prefill_gemm_kernel<<<grid, kGemmThreads, kGemmSmem, s>>>(a);
   }
   {
     cudaLaunchAttribute attr[1];
@@ -1088,34 +952,8 @@ int prefill_at(const PL& place, int B, int T, int H, int E, int r, int bits, int
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, prefill_advance_kernel<PL>, seq_lens, B, T, L_cap, place, err) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, prefill_advance_kernel, seq_lens, B, T, L_cap, err) != cudaSuccess)
       return WSVD_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
-}
-
-}  // namespace
-
-int prefill_paged(const PagedRows& place, int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
-                  const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens, uint8_t* lat_k,
-                  uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace, size_t workspace_bytes, int32_t* err,
-                  void* stream) {
-  return prefill_at(place, B, T, H, E, r, bits, L_cap, hadamard_block, x, x_dtype, A_k, A_v, seq_lens, lat_k, lat_v,
-                    scale_k, scale_v, workspace, workspace_bytes, err, stream);
-}
-
-}  // namespace wsvd
-
-extern "C" size_t wsvd_prefill_workspace_size(int B, int T, int E) {
-  if (B < 1 || T < 1 || E < 1) return 0;
-  const size_t M = (size_t)B * T;
-  return 2 * wsvd::align16(M * E * 2) + wsvd::align16(M * 4);
-}
-
-extern "C" int wsvd_latent_prefill(int B, int T, int H, int E, int r, int bits, int L_cap, int hadamard_block,
-                                   const void* x, int x_dtype, const void* A_k, const void* A_v, int32_t* seq_lens,
-                                   uint8_t* lat_k, uint8_t* lat_v, void* scale_k, void* scale_v, void* workspace,
-                                   size_t workspace_bytes, int32_t* err, void* stream) {
-  return wsvd::prefill_at(wsvd::ContiguousRows{}, B, T, H, E, r, bits, L_cap, hadamard_block, x, x_dtype, A_k, A_v,
-                          seq_lens, lat_k, lat_v, scale_k, scale_v, workspace, workspace_bytes, err, stream);
 }

@@ -112,7 +112,7 @@ def test_latent_decode_refuses(lib, kw, want):
     (dict(E=272, blk=16), 2), (dict(E=32768), 2), (dict(x=None), 1), (dict(Ak=None), 1), (dict(lens=None), 1),
     (dict(table=None), 1), (dict(sk=None), 1), (dict(ws=None), 1), (dict(x=BAD), 1), (dict(lk=BAD), 1), (dict(ws=BAD), 1),
     (dict(wsb=256), 4), (dict(out=ctypes.c_void_p(4 * MIB + 4)), 1), (dict(out=_at(5)), 1), (dict(B=0, x=None), 0),
-    (dict(T=1, r=24), 2), (dict(T=1, blk=96), 1), (dict(T=1, B=17, E=272, blk=16), 2), (dict(T=1, x=None), 1),
+    (dict(T=1, r=24), 2), (dict(r=8), 2), (dict(r=16, bits=4), 2), (dict(T=1, blk=96), 1), (dict(T=1, B=17, E=272, blk=16), 2), (dict(T=1, x=None), 1),
 ])
 def test_latent_append_refuses(lib, kw, want):
     assert lib.wsvd_latent_append_paged(*_lat_append_args(**kw)) == want
@@ -129,7 +129,7 @@ def test_workspace_sizes(lib):
     assert W.paged_decode_workspace_size(3, 4, 32, 4, 64) == size(3, 4, 32, 16, 64)
     assert W.paged_decode_workspace_size(3, 1, 16, 1, 256) == size(3, 1, 16, 8, 256)
     assert W.paged_decode_workspace_size(3, 1, 30, 8, 128) == 0
-    assert W.wsvd_latent_append_paged_workspace_size(2, 3, 256) == 256 + W.wsvd_prefill_workspace_size(2, 3, 256)
+    assert W.wsvd_latent_append_paged_workspace_size(2, 3, 256) == 256 + W.wsvd_prefill_workspace_size(2, 3, 256)  # hi, lo, scales
 
 
 def test_python_refuses_what_it_cannot_pass_on(lib):
