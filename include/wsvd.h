@@ -538,13 +538,15 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  * projected and quantised as by wsvd_latent_append, become rows seq_lens[b] ..
  * seq_lens[b] + T - 1; seq_lens_out [B] (which may be seq_lens itself) receives
  * the new lengths (fp16 factors).
- *   One token of up to 4 sequences takes wsvd_latent_append's kernel and gives
- *   its codes and scales bit for bit; so does one token of up to 16 sequences
- *   where E is no multiple of 64 or above 16384, with that call's limits.
- *   Everything else takes wsvd_latent_prefill's kernels, with that call's
- *   limits on E, r, hadamard_block and B * T; when the block is small a
- *   cluster of CTAs splits E, so that a code or scale on a rounding border may
- *   differ from the contiguous call's.
+ *   r and bits as for wsvd_decode_attention_paged (rows of 16 to 128 bytes for
+ *   int8, 16 to 64 for int4); hadamard_block a power of two in [1, 1024] that
+ *   divides E; E a multiple of 64 up to 16384, and B * T <= 2^24.  One token of
+ *   up to 16 sequences may also have another E that wsvd_latent_append takes.
+ *   One token of a few sequences (B <= 4 and B * r <= 192, or such an E) takes
+ *   that call's kernel and gives its codes and scales bit for bit.  Everything
+ *   else runs on the tensor cores with wsvd_latent_prefill's precision (x in
+ *   fp16 hi + lo halves, fp32 sums), each sum in another order, so that a code
+ *   or scale on a rounding border may differ by one step from those calls'.
  *   A sequence whose new rows do not fit in max_pages * page_size (or with
  *   seq_lens[b] < 0) raises WSVD_DEVERR_CACHE_FULL, one that needs a bad page
  *   WSVD_DEVERR_PAGE_RANGE; it is refused whole, its length kept.

@@ -584,9 +584,12 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 // one-token append's completion counter, which every call leaves zero.
 constexpr size_t kPagedCounterBytes = 256;
 
-// Sequences up to which one token each takes the append's GEMV (fp32 FMAs, up to
-// four tokens per pass over the weights) rather than the tensor-core GEMM.
-constexpr int kGemvTokens = 4;
+// Whether one token of each of B sequences takes the append's GEMV (fp32 FMAs, up
+// to four tokens per pass over the weights) rather than the tensor-core GEMM.
+// Measured, GEMV / GEMM in us, 32 heads, E 4096: r 32, 1 / 2 / 4 / 5 sequences 6.9 /
+// 7.6 / 12.3 / 17.1 against 15.5; r 64, 1 / 3 / 4 9.4 / 16.0 / 22.5 against 17.4; r 128, 1
+// / 2 / 3 14.5 / 19.6 / 34.2 against 21.8; 16 sequences of r 32 78 against 16.0.
+inline bool prefers_gemv(int B, int r) { return B <= 4 && B * r <= 192; }
 
 }  // namespace
 
@@ -694,7 +697,7 @@ extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int b
   (void)cudaGetLastError();
   // One token of few sequences, and of up to 16 where E does not suit the GEMM:
   // the append's GEMV, bound by reading A once; all else the tensor-core GEMM.
-  const cudaError_t e = gemv && (B <= kGemvTokens || !gemm)
+  const cudaError_t e = gemv && (prefers_gemv(B, r) || !gemm)
                             ? launch_append_paged(a, place, s)
                             : launch_paged_block(a, T, place, static_cast<uint8_t*>(workspace) + kPagedCounterBytes, s);
   return e == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;

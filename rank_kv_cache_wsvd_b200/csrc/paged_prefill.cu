@@ -123,21 +123,25 @@ __global__ void __launch_bounds__(512) block_rotate_kernel(const uint16_t* x, in
 }
 
 // ------------------------------------------------------------------ 2. GEMM + quantise
-constexpr int kTokens = 64, kBK = 64, kThreads = 192;
+constexpr int kTokens = 64, kBK = 64;
 
-template <int R, int BN_>
+// TG: groups of 64 tokens a tile, which share its weights.
+template <int R, int BN_, int TG_>
 struct BlockCfg {
-  static constexpr int BN = BN_;
+  static constexpr int BN = BN_, TG = TG_;
+  static constexpr int kRows = 128 * TG;                          // operand rows = epilogue threads
+  static constexpr int kThreads = kRows + 64;
   static constexpr int NG = R <= 64 ? R : 64;                    // columns per weight box
   static constexpr int SW = NG == 16 ? 6 : (NG == 32 ? 4 : 2);   // descriptor swizzle: 32 / 64 / 128 bytes
   static constexpr int HALF = kTokens * kBK * 2;                  // hi (or lo) rows of a stage
-  static constexpr int STAGE = 2 * HALF + kBK * BN * 2;
-  static constexpr int S = 6;
-  static constexpr int NH = 512 / BN;                             // accumulators: all 512 columns
+  static constexpr int WOFF = 2 * HALF * TG;                      // weights behind the token rows
+  static constexpr int STAGE = WOFF + kBK * BN * 2;
+  static constexpr int S = TG == 1 ? 6 : 4;
+  static constexpr int NH = 512 / (BN * TG);                      // accumulators: all 512 columns
   static constexpr int PITCH = BN + 4;                            // floats per row of the sums
   static constexpr int SMEM = S * STAGE + 1024 + 256;
   static_assert(R <= BN && STAGE % 1024 == 0, "whole heads; stages keep the swizzle atoms' alignment");
-  static_assert((2 * kTokens + kTokens) * PITCH * 4 <= S * STAGE, "the sums reuse the ring");
+  static_assert((TG == 1 ? 3 * kTokens : kRows) * PITCH * 4 <= S * STAGE, "the sums reuse the ring");
 };
 
 struct BlockArgs {
@@ -171,13 +175,14 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int 
 }
 
 // grid (token tiles x ranks, column tiles of K then V)
-template <int R, int BN_>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int R, int BN_, int TG_>
+__global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tm_xhi, const __grid_constant__ CUtensorMap tm_xlo,
                       const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
                       const BlockArgs a, const PagedRows place) {
-  using C = BlockCfg<R, BN_>;
-  constexpr int BN = C::BN, NG = C::NG, S = C::S, NH = C::NH;
+  using C = BlockCfg<R, BN_, TG_>;
+  constexpr int BN = C::BN, NG = C::NG, S = C::S, NH = C::NH, TG = C::TG, kThreads = C::kThreads;
+  constexpr int kProducer = C::kRows / 32, kIssuer = kProducer + 1;  // warps
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms need 1024-byte alignment
@@ -185,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::STAGE);
   uint64_t* empty = full + S;
   uint64_t* hfull = empty + S;   // [NH] a k-tile's sums are in tensor memory
-  uint64_t* hfree = hfull + NH;  // [NH] they have been read (128 arrivals)
+  uint64_t* hfree = hfull + NH;  // [NH] they have been read (an arrival per row)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(hfree + NH);
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int ranks = a.ranks, rank = (int)blockIdx.x % ranks;
-  const int m0 = (int)blockIdx.x / ranks * kTokens;
+  const int ranks = TG == 1 ? a.ranks : 1, rank = (int)blockIdx.x % ranks;
+  const int m0 = (int)blockIdx.x / ranks * (kTokens * TG);
   const int side = (int)gridDim.y / 2, kv = (int)blockIdx.y >= side, nl = ((int)blockIdx.y - kv * side) * BN;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -198,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < NH; ++i) {
       mbar_init(&hfull[i], 1);
-      mbar_init(&hfree[i], 128);
+      mbar_init(&hfree[i], C::kRows);
     }
     fence_mbar_init();
   }
-  if (warp == 5) tc05::alloc(tmem_slot, 512);
+  if (warp == kIssuer) tc05::alloc(tmem_slot, 512);
   tc05::fence_before_sync();
   __syncthreads();
   tc05::fence_after_sync();
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int kt0 = a.KT * rank / ranks, KT = a.KT * (rank + 1) / ranks - kt0;  // this rank's k-tiles
 
-  if (warp == 4) {  // ------------------------------------------------------ TMA producer
+  if (warp == kProducer) {  // ---------------------------------------------- TMA producer
     const CUtensorMap* wmap = kv ? &tm_wv : &tm_wk;
     bool waited = false;
     for (int kt = 0; kt < KT; ++kt) {
@@ -231,16 +236,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int g = 0; g < BN / NG; ++g) {
         const int col = nl + g * NG;  // heads past the last are filled with zeros
-        tma_3d(st + 2 * C::HALF + g * (kBK * NG * 2), wmap, col % R, k0, col / R, &full[s]);
+        tma_3d(st + C::WOFF + g * (kBK * NG * 2), wmap, col % R, k0, col / R, &full[s]);
       }
       if (!waited) griddep_wait();
       waited = true;
-      tma_2d(st, &tm_xhi, k0, m0, &full[s]);
-      tma_2d(st + C::HALF, &tm_xlo, k0, m0, &full[s]);
+#pragma unroll
+      for (int g = 0; g < TG; ++g) {  // tokens past the last are filled with zeros
+        tma_2d(st + 2 * g * C::HALF, &tm_xhi, k0, m0 + g * kTokens, &full[s]);
+        tma_2d(st + (2 * g + 1) * C::HALF, &tm_xlo, k0, m0 + g * kTokens, &full[s]);
+      }
     }
     for (int kt = std::max(0, KT - S); kt < KT; ++kt) wait(&full[kt % S], (uint32_t)((kt / S) & 1));
     __syncwarp();
-  } else if (warp == 5) {  // ----------------------------------------------- MMA issuer
+  } else if (warp == kIssuer) {  // ----------------------------------------- MMA issuer
     constexpr uint32_t idesc = tc05::instr_desc(1, 0, 0, 0, 1, 2 * kTokens, BN);
     for (int kt = 0; kt < KT; ++kt) {
       const int s = kt % S, hb = kt % NH;
@@ -248,11 +256,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kt >= NH) wait(&hfree[hb], (uint32_t)(((kt / NH) - 1) & 1));
       __syncwarp();
       tc05::fence_after_sync();
-      const uint32_t st = base + (uint32_t)(s * C::STAGE), d = tmem + (uint32_t)(hb * BN);
+      const uint32_t st = base + (uint32_t)(s * C::STAGE), d = tmem + (uint32_t)(hb * BN * TG);
 #pragma unroll
       for (int kk = 0; kk < kBK / 16; ++kk)
-        tc05::mma_f16_warp(d, tc05::smem_desc_sw(st + kk * 32, 16, 1024, 2),
-                           tc05::smem_desc_sw(st + 2 * C::HALF + kk * 32 * NG, 128 * NG, 16 * NG, C::SW), idesc, kk > 0);
+#pragma unroll
+        for (int g = 0; g < TG; ++g)
+          tc05::mma_f16_warp(d + (uint32_t)(g * BN), tc05::smem_desc_sw(st + 2 * g * C::HALF + kk * 32, 16, 1024, 2),
+                             tc05::smem_desc_sw(st + C::WOFF + kk * 32 * NG, 128 * NG, 16 * NG, C::SW), idesc, kk > 0);
       tc05::commit_warp(&empty[s]);
       tc05::commit_warp(&hfull[hb]);
     }
@@ -260,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kt = std::max(0, KT - NH); kt < KT; ++kt) wait(&hfull[kt % NH], (uint32_t)((kt / NH) & 1));
     __syncwarp();
   } else {  // ---------------------------------------------------------------- thread = operand row
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp >> 2) * BN);
     float tot[BN];
 #pragma unroll
     for (int c = 0; c < BN; ++c) tot[c] = 0.f;
@@ -271,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c0 = 0; c0 < BN; c0 += 64) {  // two loads in flight per wait
         uint32_t va[32], vb[32];
-        tc05::ld32(lane_base + (uint32_t)(hb * BN + c0), va);
-        tc05::ld32(lane_base + (uint32_t)(hb * BN + c0 + 32), vb);
+        tc05::ld32(lane_base + (uint32_t)(hb * BN * TG + c0), va);
+        tc05::ld32(lane_base + (uint32_t)(hb * BN * TG + c0 + 32), vb);
         tc05::wait_ld();
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&hfree[hb]);
     }
     griddep_wait();  // 1 / p comes from the rotation grid
-    const int m = m0 + (tid & (kTokens - 1));
+    const int m = m0 + (tid >> 7) * kTokens + (tid & (kTokens - 1));
     const float ip = m < a.M ? a.inv_p[m] : 0.f;
     float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + (size_t)tid * C::PITCH);
 #pragma unroll
@@ -294,20 +304,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the rank's share of the tokens: hi and lo of all ranks, in order
   cg::cluster_group cluster = cg::this_cluster();
-  float* part = reinterpret_cast<float*>(smem);        // [hi 64, lo 64][PITCH]
-  float* sums = part + 2 * kTokens * C::PITCH;          // [tokens of this rank][PITCH]
-  const int r0 = kTokens * rank / ranks, rows = kTokens * (rank + 1) / ranks - r0;
+  float* part = reinterpret_cast<float*>(smem);  // per group [hi 64, lo 64][PITCH]
+  // The joined tokens [PITCH]: behind the parts that other ranks read, else over the hi rows.
+  float* sums = ranks > 1 ? part + 2 * kTokens * C::PITCH : part;
+  const int r0 = kTokens * rank / ranks, rows = ranks > 1 ? kTokens * (rank + 1) / ranks - r0 : kTokens * TG;
+  auto at_row = [&](int row) { return (size_t)(ranks > 1 ? row : (row >> 6) * 128 + (row & 63)) * C::PITCH; };
   if (ranks > 1) cluster.sync();
   else __syncthreads();
   for (int i = tid; i < rows * (BN / 4); i += kThreads) {
     const int row = i / (BN / 4), c = i % (BN / 4) * 4;
     if (m0 + r0 + row >= a.M) break;
-    const size_t hi = (size_t)(r0 + row) * C::PITCH + c, lo = hi + (size_t)kTokens * C::PITCH;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (ranks == 1) {
-      const float4 x = *reinterpret_cast<const float4*>(part + hi), y = *reinterpret_cast<const float4*>(part + lo);
+      const float* p = part + at_row(row) + c;
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      const float4 y = *reinterpret_cast<const float4*>(p + (size_t)kTokens * C::PITCH);
       v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
     } else {
+      const size_t hi = (size_t)(r0 + row) * C::PITCH + c, lo = hi + (size_t)kTokens * C::PITCH;
       float4 x[8], y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           v = make_float4(v.x + (x[q].x + y[q].x), v.y + (x[q].y + y[q].y), v.z + (x[q].z + y[q].z),
                           v.w + (x[q].w + y[q].w));
     }
-    *reinterpret_cast<float4*>(sums + (size_t)row * C::PITCH + c) = v;
+    *reinterpret_cast<float4*>(sums + at_row(row) + c) = v;
   }
   if (ranks > 1) cluster.sync();  // the ranks' sums have been read: a rank may leave
   else __syncthreads();
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int u = tid; u < (units + 31) / 32 * 32; u += kThreads) {  // whole warps: the maximum crosses lanes
     const int row = u / (HEADS * LPU), hh = u / LPU % HEADS, sub = u % LPU, m = m0 + r0 + row, h = nl / R + hh;
     const bool real = u < units && m < a.M && h < a.H;
-    const float4* src = reinterpret_cast<const float4*>(sums + (size_t)(u < units ? row : 0) * C::PITCH + hh * R + sub * COLS);
+    const float4* src = reinterpret_cast<const float4*>(sums + at_row(u < units ? row : 0) + hh * R + sub * COLS);
     float v[COLS], amax = 0.f;
 #pragma unroll
     for (int c = 0; c < COLS / 4; ++c) {
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc05::fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kIssuer) {
     tc05::fence_after_sync();
     tc05::dealloc(tmem, 512);
   }
@@ -442,7 +456,7 @@ bool weight_map(CUtensorMap* tm, const void* base, int H, int E, int r, int NG) 
 // Clusters of c CTAs of a kernel that the current device runs at once (the
 // shared-memory opt-in is made on the way; asked once per device, kernel and
 // size; 0 on failure).
-int resident_clusters(const void* kern, size_t smem, int c) {
+int resident_clusters(const void* kern, int threads, size_t smem, int c) {
   static std::mutex mu;
   static std::map<std::tuple<int, const void*, int>, int> known;
   int dev = 0, n = 0;
@@ -453,7 +467,7 @@ int resident_clusters(const void* kern, size_t smem, int c) {
   if (it != known.end()) return it->second;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)c);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -470,23 +484,23 @@ int resident_clusters(const void* kern, size_t smem, int c) {
   return known[key] = n;
 }
 
-template <int R, int BN>
-cudaError_t launch_block(BlockArgs a, const __half* xhi, const __half* xlo, int E, const void* A_k, const void* A_v,
+template <int R, int BN, int TG>
+cudaError_t launch_tiles(BlockArgs a, const __half* xhi, const __half* xlo, int E, const void* A_k, const void* A_v,
                          const PagedRows& place, cudaStream_t s) {
-  using C = BlockCfg<R, BN>;
-  auto kern = block_gemm_kernel<R, BN>;
+  using C = BlockCfg<R, BN, TG>;
+  auto kern = block_gemm_kernel<R, BN, TG>;
   const void* fn = reinterpret_cast<const void*>(kern);
   CUtensorMap mh, ml, mk, mv;
   if (!token_map(&mh, xhi, a.M, E) || !token_map(&ml, xlo, a.M, E) || !weight_map(&mk, A_k, a.H, E, R, C::NG) ||
       !weight_map(&mv, A_v, a.H, E, R, C::NG))
     return cudaErrorInvalidValue;
-  if (resident_clusters(fn, C::SMEM, 1) < 1) return cudaErrorInvalidConfiguration;
-  const int mt = (a.M + kTokens - 1) / kTokens, nt = 2 * ((a.H * R + BN - 1) / BN);
+  if (resident_clusters(fn, C::kThreads, C::SMEM, 1) < 1) return cudaErrorInvalidConfiguration;
+  const int mt = (a.M + kTokens * TG - 1) / (kTokens * TG), nt = 2 * ((a.H * R + BN - 1) / BN);
   a.KT = E / kBK;
   // The most ranks whose clusters all run at once, at least two k-tiles each.
   a.ranks = 1;
-  for (int c = 8; c > 1 && a.ranks == 1; c >>= 1)
-    if (2 * c <= a.KT && (long long)mt * nt <= resident_clusters(fn, C::SMEM, c)) a.ranks = c;
+  for (int c = 8; TG == 1 && c > 1 && a.ranks == 1; c >>= 1)
+    if (2 * c <= a.KT && (long long)mt * nt <= resident_clusters(fn, C::kThreads, C::SMEM, c)) a.ranks = c;
   a.ctas = mt * a.ranks * nt;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -497,12 +511,25 @@ cudaError_t launch_block(BlockArgs a, const __half* xhi, const __half* xlo, int 
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(mt * a.ranks), (unsigned)nt);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, mh, ml, mk, mv, a, place);
+}
+
+// Tiles of 64 tokens where they fit one wave of CTAs; past that tiles of 128,
+// whose weights are fetched once for twice the tokens (a tile of 128 takes about
+// 1.75 times one of 64), unless they leave the last wave emptier.
+template <int R, int BN>
+cudaError_t launch_block(const BlockArgs& a, const __half* xhi, const __half* xlo, int E, const void* A_k,
+                         const void* A_v, const PagedRows& place, cudaStream_t s) {
+  const int nt = 2 * ((a.H * R + BN - 1) / BN), sms = 148;
+  const int waves1 = ((a.M + 63) / 64 * nt + sms - 1) / sms, waves2 = ((a.M + 127) / 128 * nt + sms - 1) / sms;
+  if (BN == 128 && waves1 > 1 && 7 * waves2 <= 4 * waves1)
+    return launch_tiles<R, BN, BN == 128 ? 2 : 1>(a, xhi, xlo, E, A_k, A_v, place, s);
+  return launch_tiles<R, BN, 1>(a, xhi, xlo, E, A_k, A_v, place, s);
 }
 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
