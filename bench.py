@@ -68,7 +68,8 @@ def source_digest(files):
     return h.hexdigest()[:16]
 
 
-KERNEL_SOURCES = {"append": ["append.cu", "append_core.cuh", "common.cuh", "wsvd_internal.h", "api.cu"],
+KERNEL_SOURCES = {"append": ["append.cu", "append_core.cuh", "paged_rows.cuh", "common.cuh", "wsvd_internal.h",
+                             "api.cu"],
                   "step": ["decode.cu", "append_core.cuh", "common.cuh", "wsvd_internal.h", "api.cu"],
                   "decode": ["decode.cu", "shared.cu", "common.cuh", "wsvd_internal.h", "api.cu"],
                   "prefill_gemm": ["prefill.cu", "common.cuh", "wsvd_internal.h", "tc05.cuh"],

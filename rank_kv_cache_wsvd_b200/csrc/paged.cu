@@ -97,6 +97,7 @@ constexpr int kAppendRows = 6;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArgs a) {
+  griddep_wait();
   const int b = blockIdx.y, tid = threadIdx.x;
   const int units = a.Hd / 16, rows = a.Hq + 2 * a.Hkv, ru = a.rot / 16;
   const int unit = tid & (units - 1), slot = tid / units;
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c4 = lane & 3;
   const int c = blockIdx.x;
   const PagedSeqs& seqs = a.seqs;
+  griddep_wait();
 
   // Sequences without rows: zeros, spread over the CTAs.
   for (int b = c; b < seqs.B; b += gridDim.x)
@@ -827,9 +829,8 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
   const int tokens = slots / a.row_slots;
   const dim3 grid((unsigned)std::max(1, (T + tokens - 1) / tokens), (unsigned)B);
   (void)cudaGetLastError();
-  if (dtype == WSVD_DTYPE_BF16) kv_append_kernel<true><<<grid, kAppendCta, 0, as_stream(stream)>>>(a);
-  else kv_append_kernel<false><<<grid, kAppendCta, 0, as_stream(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+  const auto kern = dtype == WSVD_DTYPE_BF16 ? kv_append_kernel<true> : kv_append_kernel<false>;
+  return launch_behind(kern, grid, kAppendCta, 0, as_stream(stream), a) == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
 }
 
 size_t paged_decode_workspace_size(int B, int Tq, int Hq, int Hkv, int Hd) {
@@ -869,8 +870,9 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
   (void)cudaGetLastError();
   if (paged_resident_ctas(reinterpret_cast<const void*>(kern.fn), kern.threads, kern.smem, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
-  kern.fn<<<a.ctas, kern.threads, kern.smem, as_stream(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? WSVD_OK : WSVD_ERR_CUDA;
+  return launch_behind(kern.fn, dim3((unsigned)a.ctas), kern.threads, kern.smem, as_stream(stream), a) == cudaSuccess
+             ? WSVD_OK
+             : WSVD_ERR_CUDA;
 }
 
 }  // extern "C"

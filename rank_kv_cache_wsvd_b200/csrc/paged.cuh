@@ -2,6 +2,8 @@
 // CTAs, the warp's copies, and host helpers of the entry points.
 #pragma once
 
+#include <utility>
+
 #include "common.cuh"
 
 namespace wsvd {
@@ -141,6 +143,24 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 }
 
 // ------------------------------------------------------------------ host
+// Launches a kernel that begins with griddep_wait: its CTAs may be placed while
+// the stream's preceding kernel drains, and touch no memory before that one has
+// completed (two calls in a row 2 us sooner than with an ordinary launch).
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+
 // Upper bound of the paged decodes' grids; sizes their partial results.
 constexpr int kMaxPagedCtas = 592;
 

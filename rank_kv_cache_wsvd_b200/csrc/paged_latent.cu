@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
   const PagedSeqs& seqs = a.seqs;
   // Worker: one warp.  Few workers are spread over the SMs.
   const int me = warp * gridDim.x + blockIdx.x;
+  griddep_wait();
 
   for (int b = blockIdx.x; b < seqs.B; b += gridDim.x)
     if (seqs.rows(b) == 0)
@@ -550,14 +551,14 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
 }
 
 struct LatKernel {
-  const void* fn;
+  void (*fn)(const LatDecodeArgs);
   size_t smem;
   int threads;
 };
 template <int BITS, int RB>
 LatKernel lat_kernel() {
   using C = LatCfg<BITS, RB>;
-  return LatKernel{reinterpret_cast<const void*>(&lat_decode_kernel<BITS, RB>), C::kSmem, C::kThreads};
+  return LatKernel{&lat_decode_kernel<BITS, RB>, C::kSmem, C::kThreads};
 }
 bool pick_lat(int bits, int rowbytes, LatKernel* k) {
   if (bits == 8) {
@@ -636,11 +637,9 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();
-  if (paged_resident_ctas(kern.fn, kern.threads, kern.smem, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
-  void* args[] = {&a};
-  return cudaLaunchKernel(kern.fn, dim3((unsigned)a.ctas), dim3((unsigned)kern.threads), args, kern.smem, s) == cudaSuccess
-             ? WSVD_OK
-             : WSVD_ERR_CUDA;
+  if (paged_resident_ctas(reinterpret_cast<const void*>(kern.fn), kern.threads, kern.smem, &a.ctas) != cudaSuccess) return WSVD_ERR_CUDA;
+  return launch_behind(kern.fn, dim3((unsigned)a.ctas), kern.threads, kern.smem, s, a) == cudaSuccess ? WSVD_OK
+                                                                                                       : WSVD_ERR_CUDA;
 }
 
 extern "C" size_t wsvd_latent_append_paged_workspace_size(int B, int T, int E) {

@@ -33,6 +33,7 @@
 #include <tuple>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "paged_rows.cuh"
 #include "tc05.cuh"
 
@@ -48,6 +49,7 @@ template <int EPT>
 __global__ void __launch_bounds__(512) block_rotate_kernel(const uint16_t* x, int dtype, int E, int blk, float hnorm,
                                                            __half* xhi, __half* xlo, float* inv_p) {
   __shared__ float wmax[16];
+  griddep_wait();
   griddep_launch_dependents();  // the GEMM may set up (it waits for this grid before it reads)
   const int tid = threadIdx.x, lane = tid & 31, e = tid * EPT;
   const size_t at = (size_t)blockIdx.x * E + e;
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
   uint64_t* hfull = empty + S;   // [NH] a k-tile's sums are in tensor memory
   uint64_t* hfree = hfull + NH;  // [NH] they have been read (an arrival per row)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(hfree + NH);
+  __shared__ int sm_pos[kTokens * TG], sm_why[kTokens * TG];  // of the tile's tokens: first row of its block, refusal
   const int tid = threadIdx.x, warp = tid >> 5;
   const int ranks = TG == 1 ? a.ranks : 1, rank = (int)blockIdx.x % ranks;
   const int m0 = (int)blockIdx.x / ranks * (kTokens * TG);
@@ -271,6 +274,13 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     __syncwarp();
   } else {  // ---------------------------------------------------------------- thread = operand row
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp >> 2) * BN);
+    const int token = (tid >> 7) * kTokens + (tid & (kTokens - 1)), m = m0 + token;
+    if ((tid & 127) < kTokens && m < a.M) {  // while the first tiles arrive
+      const int b = m / a.T, pos = ld_relaxed_gpu(a.seq_lens + b);
+      sm_pos[token] = pos;
+      sm_why[token] = place.refused(b, pos, a.T, a.cap);
+    }
+    __syncwarp();
     float tot[BN];
 #pragma unroll
     for (int c = 0; c < BN; ++c) tot[c] = 0.f;
@@ -294,7 +304,6 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
       mbar_arrive(&hfree[hb]);
     }
     griddep_wait();  // 1 / p comes from the rotation grid
-    const int m = m0 + (tid >> 7) * kTokens + (tid & (kTokens - 1));
     const float ip = m < a.M ? a.inv_p[m] : 0.f;
     float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + (size_t)tid * C::PITCH);
 #pragma unroll
@@ -359,8 +368,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
 #pragma unroll
     for (int o = LPU / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (!real) continue;
-    const int b = m / a.T, t = m - b * a.T, pos = ld_relaxed_gpu(a.seq_lens + b);
-    const int why = place.refused(b, pos, a.T, a.cap);
+    const int b = m / a.T, t = m - b * a.T, pos = sm_pos[r0 + row], why = sm_why[r0 + row];
     if (why) {
       if (blockIdx.y == 0 && hh == 0 && sub == 0 && t == 0) set_err(a.err, why);
       continue;
@@ -557,13 +565,10 @@ cudaError_t launch_paged_block(const AppendArgs& p, int T, const PagedRows& plac
   int ept = 4;
   while (ept * 32 < p.blk || ept * 512 < p.E) ept *= 2;
   const unsigned nt = (unsigned)((p.E / ept + 31) / 32 * 32);
-  switch (ept) {
-    case 4: block_rotate_kernel<4><<<M, nt, 0, s>>>(x, p.x_dtype, p.E, p.blk, p.hnorm, xhi, xlo, inv); break;
-    case 8: block_rotate_kernel<8><<<M, nt, 0, s>>>(x, p.x_dtype, p.E, p.blk, p.hnorm, xhi, xlo, inv); break;
-    case 16: block_rotate_kernel<16><<<M, nt, 0, s>>>(x, p.x_dtype, p.E, p.blk, p.hnorm, xhi, xlo, inv); break;
-    default: block_rotate_kernel<32><<<M, nt, 0, s>>>(x, p.x_dtype, p.E, p.blk, p.hnorm, xhi, xlo, inv); break;
-  }
-  cudaError_t e = cudaGetLastError();
+  const auto rotate = ept == 4 ? block_rotate_kernel<4> : ept == 8 ? block_rotate_kernel<8>
+                      : ept == 16 ? block_rotate_kernel<16> : block_rotate_kernel<32>;
+  const cudaError_t e = launch_behind(rotate, dim3((unsigned)M), (int)nt, 0, s, x, p.x_dtype, p.E, p.blk, p.hnorm, xhi,
+                                      xlo, inv);
   if (e != cudaSuccess) return e;
   BlockArgs a{};
   a.M = M; a.T = T; a.B = p.B; a.H = p.H; a.bits = p.bits; a.cap = p.L_cap;

@@ -350,6 +350,43 @@ def test_latent_append_and_decode_as_used():
     assert (ws[:256] == 0).all()
 
 
+def test_latent_block_append_in_a_graph():
+    """A captured block of tokens (two launches, tensor maps among their
+    arguments) replays on new contents and lengths, and on two streams at once
+    with a workspace each."""
+    B, T, H, E, r, page = 2, 24, 8, 512, 32, 16
+    table, pool = table_for([128] * B, page, 4)
+    Ak, Av = _down(H, E, r, 1)
+    x, n = _x(B, T, E, 2), torch.zeros(B, dtype=torch.int32, device="cuda")
+    tab = cuda(table)
+    ws = W.workspace(W.wsvd_latent_append_paged_workspace_size(B, T, E))
+    cache = _empty(pool, H, r, 8, page, 3)
+    err, graph = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        W.wsvd_latent_append_paged(x, Ak, Av, n, tab, *cache, 8, 128, workspace_buf=ws, err=err)
+    lens = [0] * B
+    for i in range(3):
+        x.copy_(_x(B, T, E, 10 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_rows(*cache, table, lens, x, Ak, Av, 8, page, 128)
+        lens = [a + T for a in lens]
+        assert n.tolist() == lens and int(err.item()) == 0
+    other = [t.clone() for t in cache]
+    n1, n2 = torch.zeros_like(n), torch.zeros_like(n)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        n1.zero_(), n2.zero_()
+        torch.cuda.synchronize()
+        W.wsvd_latent_append_paged(x, Ak, Av, n1, tab, *cache, 8, 128, stream=s1)
+        W.wsvd_latent_append_paged(x, Ak, Av, n2, tab, *other, 8, 128, stream=s2)
+        torch.cuda.synchronize()
+        assert n1.tolist() == n2.tolist() == [T] * B
+    for a, b in zip(cache, other):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_latent_append_of_no_tokens_copies_the_lengths():
     H, E, r, page = 2, 256, 16, 16
     table, pool = table_for([64] * 2, page, 5)
