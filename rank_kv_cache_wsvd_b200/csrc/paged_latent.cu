@@ -128,9 +128,9 @@ __device__ __forceinline__ uint32_t bytes_of(const uint4& w, uint32_t sel) {
 }
 
 // A warp's q' = bk . q, bk [R][Hd] fp16, Hd <= 64 N: eight lanes to a row, four
-// rows at a time.  Returns the lane's largest |q'|.
+// rows at a time.  Returns the lane's largest |q'| as bits (a NaN above all).
 template <int R, int N>
-__device__ __forceinline__ float project_query(const uint16_t* q, int dtype, const __half* bk, int Hd, float* out,
+__device__ __forceinline__ int project_query(const uint16_t* q, int dtype, const __half* bk, int Hd, float* out,
                                                int lane) {
   const int sub = lane & 7, part = lane >> 3;
   float x[N][8];
@@ -149,7 +149,7 @@ __device__ __forceinline__ float project_query(const uint16_t* q, int dtype, con
       x[i][2 * k + 1] = f.y;
     }
   }
-  float amax = 0.f;
+  int amax = 0;
   constexpr int kFly = R / 4 < 8 ? R / 4 : (N == 4 ? 4 : 8);  // turns whose loads are in flight together
 #pragma unroll 1
   for (int j0 = 0; j0 < R; j0 += 4 * kFly) {
@@ -178,7 +178,7 @@ __device__ __forceinline__ float project_query(const uint16_t* q, int dtype, con
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (sub == 0) out[j0 + 4 * j + part] = v;
-      amax = fmaxf(amax, fabsf(v));
+      amax = max(amax, __float_as_int(fabsf(v)));
     }
   }
   return amax;
@@ -310,10 +310,10 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
     {
       const uint16_t* q = a.q + bh * Hd;
       const __half* bk = a.Bk + (size_t)h * R * Hd;
-      float amax = Hd == 128  ? project_query<R, 2>(q, a.q_dtype, bk, Hd, sm_q[warp], lane)
-                   : Hd == 256 ? project_query<R, 4>(q, a.q_dtype, bk, Hd, sm_q[warp], lane)
-                               : project_query<R, 1>(q, a.q_dtype, bk, Hd, sm_q[warp], lane);
-      amax = key_float(warp_max_s32(float_key(amax)));
+      const int most = Hd == 128  ? project_query<R, 2>(q, a.q_dtype, bk, Hd, sm_q[warp], lane)
+                       : Hd == 256 ? project_query<R, 4>(q, a.q_dtype, bk, Hd, sm_q[warp], lane)
+                                   : project_query<R, 1>(q, a.q_dtype, bk, Hd, sm_q[warp], lane);
+      const float amax = __int_as_float(warp_max_s32(most));
       __syncwarp();
       const float inv = amax > 0.f ? (float)kDigitMax / amax : 0.f;
       qstep = amax / (float)kDigitMax * a.qscale * (BITS == 4 ? 0.0625f : 1.f);

@@ -126,6 +126,27 @@ def test_latent_decode_extreme_codes_and_scales():
         _check(out, q, cache, Bk, Bv, lens, bits, what=f"extreme int{bits}")
 
 
+def test_latent_decode_nan_stays_where_it_is_seen():
+    """A NaN query or a NaN scale of a visible row makes that head's output NaN
+    and no other's."""
+    lens, H = [130, 40], 3
+    for bits, r in RANKS:
+        cache = _cache(lens, H, r, bits, 16, seed=5, poison=False)
+        lk, lv, sk, sv, table = cache
+        Bk, Bv = _factors(H, r, 64, 6)
+        q = randn((2, H, 64), "bf16", 7)
+        good, _ = _decode(q, cache, Bk, Bv, lens, bits)
+        q2, sk2, sv2 = q.clone(), sk.clone(), sv.clone()
+        q2[0, 1, 5] = float("nan")
+        sk2[table[0, 3], 2, 7] = float("nan")
+        sv2[table[1, 2], 0, 7] = float("nan")   # row 39 of sequence 1
+        bad, err = _decode(q2, (lk, lv, sk2, sv2, table), Bk, Bv, lens, bits)
+        assert err == 0
+        hit = torch.zeros((2, H), dtype=torch.bool, device="cuda")
+        hit[0, 1] = hit[0, 2] = hit[1, 0] = True
+        assert torch.isnan(bad[hit]).all() and torch.equal(bad[~hit], good[~hit])
+
+
 def test_latent_decode_matches_the_contiguous_one():
     """The same rows in pages and contiguous: both agree with the float64 value
     under the framework's rule (1e-3 of the largest output, plus 1e-5)."""

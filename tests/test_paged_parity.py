@@ -125,6 +125,26 @@ def test_decode_rows_a_query_does_not_see_never_reach_it(dtype, Hd, bad):
     assert (np.abs(got.double().cpu().numpy() - ref[:, :2]) <= allow).all()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_decode_nan_stays_where_it_is_seen(dtype):
+    """A NaN query makes its own output NaN; a NaN key or value of a visible row
+    those of its KV head."""
+    lens = [70, 33]
+    kp, vp, table = _cache(lens, 3, 64, 16, dtype, seed=5)
+    q = randn((2, 1, 12, 64), dtype, 6)
+    good, _ = _decode(q, kp, vp, table, lens)
+    q2, kp2, vp2 = q.clone(), kp.clone(), vp.clone()
+    q2[0, 0, 5, 9] = NAN
+    kp2[table[0, 2], 2, 3, 1] = NAN
+    vp2[table[1, 2], 0, 0, 17] = NAN  # row 32 of sequence 1
+    bad, err = _decode(q2, kp2, vp2, table, lens)
+    assert err == 0
+    hit = torch.zeros_like(good, dtype=torch.bool)
+    hit[0, 0, 5] = hit[0, 0, 8:12] = True
+    hit[1, 0, 0:4, 17] = True
+    assert torch.isnan(bad[hit]).all() and torch.equal(bad[~hit], good[~hit])
+
+
 def test_decode_shared_prefix_pages():
     lens = [100, 90, 64]
     table, pool = table_for(lens, 32, 3, shared=2)
