@@ -250,7 +250,7 @@ struct KvDecodeArgs {
   const int32_t* block_table;
   const uint16_t *q, *k, *v;
   float* out;
-  float* partials;  // [2 * ctas] of O [min(nq, kQ)][HD], then (m, l) per query
+  float* partials;  // two a worker: O [min(nq, kQ)][HD], then (m, l) per query
   int32_t* counters;
   int32_t* err;
   float qscale;
@@ -290,7 +290,18 @@ __device__ __forceinline__ uint32_t strip_off(int r, int c) {
 // heads of 1600 rows 12.4 / 11.7 / 10.6 / 10.6 us.
 constexpr int kLead = 24;
 
-template <bool BF16, int HD, int NB>
+// Up to 8 queries a head, many units and sequences of few strips: every warp is a
+// worker with segments of its own, nothing waits for a CTA, and most units end in
+// one warp's registers.  Measured with CTAs / warps as workers (us; 8 heads of
+// 128, 4 queries each): 256 x 128 rows 56.4 / 36.7, 64 x 1..300 rows 23.5 / 20.4, 64 x
+// 500 33.8 / 33.7, 32 x 1000 30.2 / 33.8; one sequence of 300 rows, whose few units
+// warps would have to join, 7.8 / 15.
+constexpr int kSoloStrips = 32, kSoloUnits = 512, kSoloLead = 4;
+constexpr int kMaxSolo = 2048;  // workers that way at most; sizes the partials
+
+// MANY: many units, so that their sequences may be short (kSoloUnits); a kernel of
+// its own, as the code alone costs a small call half a microsecond.
+template <bool BF16, int HD, int NB, bool MANY>
 __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_kernel(const KvDecodeArgs a) {
   using C = DecCfg<BF16, HD, NB>;
   constexpr int TS = C::kTS, MT = C::kMT, S = C::kStages, NW = C::kWarps, KS = HD / 16, NP = C::kParts;
@@ -309,21 +320,30 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   for (int b = c; b < seqs.B; b += gridDim.x)
     if (seqs.rows(b) == 0)
       for (int i = tid; i < a.Tq * a.Hq * HD; i += C::kThreads) a.out[(size_t)b * a.Tq * a.Hq * HD + i] = 0.f;
-  Strips<TS, kLead> share;
-  typename Strips<TS, kLead>::Segment seg;
-  if (!share.deal(seqs, c, a.ctas, NW, a.err, &seg)) return;
+  Strips<TS> share;
+  typename Strips<TS>::Segment seg;
+  bool solo = false;  // short sequences: every warp a worker of its own
+  int me = c;
+  const auto plan = [&](int mean, int live) {
+    solo = MANY && mean < kSoloStrips && live * (long long)seqs.units >= kSoloUnits;
+    if (!solo) return typename Strips<TS>::Plan{c, a.ctas, NW, kLead};
+    me = warp * (int)gridDim.x + c;
+    return typename Strips<TS>::Plan{me, min((int)gridDim.x * NW, kMaxSolo), 1, kSoloLead};
+  };
+  if (!share.deal(seqs, plan, a.err, &seg)) return;
+  const int first = MANY && solo ? 0 : warp, stride = MANY && solo ? 1 : NW;  // of a segment's strips, this warp's
 
   // ---- the warp's copies: cursor `ld`, page ids one strip ahead
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
   auto ld = seg;
-  int ls = ld.s + warp;
+  int ls = ld.s + first;
   bool more = true;
   int pg[MT];
   const int page_mask = (1 << a.page_shift) - 1;
   auto settle = [&]() {  // the next strip of this warp, and its pages
     while (more && ls >= ld.e) {
       more = ld.next(seqs);
-      ls = ld.s + warp;
+      ls = ld.s + first;
     }
     if (more) {
 #pragma unroll
@@ -358,7 +378,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
         }
       }
       if (lane == 0) sm_valid[warp][stage] = valid;
-      ls += NW;
+      ls += stride;
       settle();
     }
     cp_commit();
@@ -398,7 +418,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     }
 
     int last_stage = stage == 0 ? S - 1 : stage - 1;  // a stage with nothing in it or on its way
-    for (int s = seg.s + warp; s < seg.e; s += NW) {
+    for (int s = seg.s + first; s < seg.e; s += stride) {
       cp_wait<S - 2>();
       __syncwarp();
       issue(stage == 0 ? S - 1 : stage - 1);
@@ -572,6 +592,93 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
       stage = stage == S - 1 ? 0 : stage + 1;
     }
 
+    const bool whole = seg.s == 0 && seg.e == seg.strips();
+    const int qmax = min(C::kQ, a.nq);  // queries per partial slot
+    const int slot = partial_floats(qmax, HD);
+    // A worker has at most one unit that it begins within, and one that it only begins.
+    float* part = a.partials + (size_t)(2 * me + (seg.s == 0 ? 1 : 0)) * slot;
+    const size_t unit = (size_t)seg.b * seqs.units + seg.u;
+    auto store = [&](int j, int d, float4 v, float L) {
+      const int jq = j0 + j, t = jq / a.G;
+      const float f = lim_min + t > 0 ? 1.f / L : 0.f;
+      if (f == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(a.out + (((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d) =
+          make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    };
+    // Joins the partials of a unit's workers, in their order; idx0, step: the
+    // caller's threads.
+    auto join = [&](int idx0, int step) {
+      int wf, np;
+      share.holders(seg, &wf, &np);
+      const float* from = a.partials + (size_t)2 * wf * slot;
+      constexpr int kJoin = 8;  // partials whose loads are in flight together
+      for (int idx = idx0; idx < nq * (HD / 4); idx += step) {
+        const int j = idx / (HD / 4), d = idx % (HD / 4) * 4;
+        float M = kNegInf, L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < np; i0 += kJoin) {
+          float2 ml[kJoin];
+          float4 x[kJoin];
+          float top = M;
+#pragma unroll
+          for (int i = 0; i < kJoin; ++i) {
+            const float* p = from + (size_t)2 * (i0 + i) * slot + (i0 + i == 0 ? slot : 0);  // slot 1 of the first
+            const bool in = i0 + i < np;
+            ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + qmax * HD + 2 * j)) : make_float2(kNegInf, 0.f);
+            x[i] = in ? __ldcg(reinterpret_cast<const float4*>(p + j * HD + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int i = 0; i < kJoin; ++i) top = fmaxf(top, ml[i].x);
+          const float ref = top == kNegInf ? 0.f : top, f0 = ex2(M - ref);
+          L *= f0;
+          v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+#pragma unroll
+          for (int i = 0; i < kJoin; ++i) {
+            const float f = ex2(ml[i].x - ref);
+            L = fmaf(ml[i].y, f, L);
+            v.x = fmaf(x[i].x, f, v.x);
+            v.y = fmaf(x[i].y, f, v.y);
+            v.z = fmaf(x[i].z, f, v.z);
+            v.w = fmaf(x[i].w, f, v.w);
+          }
+          M = top;
+        }
+        store(j, d, v, L);
+      }
+    };
+
+    if (MANY && solo) {  // ---- one warp's result: straight to out, or to its partial slot
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float L = l[0][i];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+        const int j = 2 * c4 + i;
+        if (j >= nq) continue;
+        const int jq = j0 + j, t = jq / a.G;
+        float* to = whole ? a.out + (((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD : part + j * HD;
+        const bool sees = lim_min + t > 0;
+        const float f = whole ? 1.f / L : 1.f;
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+          __stcg(to + d * 16 + g, whole && !sees ? 0.f : o[d][0][i] * f);
+          __stcg(to + d * 16 + 8 + g, whole && !sees ? 0.f : o[d][0][2 + i] * f);
+        }
+        if (!whole && g == 0) __stcg(reinterpret_cast<float2*>(part + qmax * HD + 2 * j), make_float2(m[0][i], L));
+      }
+      if (whole) continue;
+      int wf, np, last = 0;
+      share.holders(seg, &wf, &np);
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) last = atom_add_acq_rel_gpu(a.counters + unit, 1) == np - 1;
+      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+      __threadfence();
+      join(lane, 32);
+      if (lane == 0) st_relaxed_gpu(a.counters + unit, 0);
+      continue;
+    }
+
     // ---- the warps' results of this segment, joined.  Each warp leaves O in
     // its free stage, [query][dim] with bits 3 and 4 of dim turned by the lane
     // so that the stores meet no bank twice and float4 reads stay whole.
@@ -596,19 +703,6 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
       }
     if (lane == 0) sm_slot[warp] = warp * S + last_stage;
     __syncthreads();
-    const int ns = seg.strips();
-    const bool whole = seg.s == 0 && seg.e == ns;
-    const int qmax = min(C::kQ, a.nq);  // queries per partial slot
-    const int slot = partial_floats(qmax, HD);
-    // A CTA has at most one unit that it begins within, and one that it only begins.
-    float* part = a.partials + (size_t)(2 * c + (seg.s == 0 ? 1 : 0)) * slot;
-    auto store = [&](int j, int d, float4 v, float L) {
-      const int jq = j0 + j, t = jq / a.G;
-      const float f = lim_min + t > 0 ? 1.f / L : 0.f;
-      if (f == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(a.out + (((size_t)seg.b * a.Tq + t) * a.Hq + h * a.G + jq % a.G) * HD + d) =
-          make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-    };
     for (int idx = tid; idx < nq * (HD / 4); idx += C::kThreads) {
       const int j = idx / (HD / 4), d = idx % (HD / 4) * 4;
       float M = kNegInf, L = 0.f;
@@ -639,50 +733,15 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     // ---- a unit cut over several CTAs: the last to arrive joins the partials
     // in the order of the CTAs, so the result does not depend on who that is.
     if (!whole) {
-      int cf, np;
-      share.holders(seg, &cf, &np);
-      const size_t unit = (size_t)seg.b * seqs.units + seg.u;
+      int wf, np;
+      share.holders(seg, &wf, &np);
       __threadfence();
       __syncthreads();
       if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + unit, 1) == np - 1;
       __syncthreads();
       if (sm_last) {
         __threadfence();
-        const float* from = a.partials + (size_t)2 * cf * slot;
-        constexpr int kJoin = 8;  // partials whose loads are in flight together
-        for (int idx = tid; idx < nq * (HD / 4); idx += C::kThreads) {
-          const int j = idx / (HD / 4), d = idx % (HD / 4) * 4;
-          float M = kNegInf, L = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int i0 = 0; i0 < np; i0 += kJoin) {
-            float2 ml[kJoin];
-            float4 x[kJoin];
-            float top = M;
-#pragma unroll
-            for (int i = 0; i < kJoin; ++i) {
-              const float* p = from + (size_t)2 * (i0 + i) * slot + (i0 + i == 0 ? slot : 0);  // slot 1 of the first CTA
-              const bool in = i0 + i < np;
-              ml[i] = in ? __ldcg(reinterpret_cast<const float2*>(p + qmax * HD + 2 * j)) : make_float2(kNegInf, 0.f);
-              x[i] = in ? __ldcg(reinterpret_cast<const float4*>(p + j * HD + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int i = 0; i < kJoin; ++i) top = fmaxf(top, ml[i].x);
-            const float ref = top == kNegInf ? 0.f : top, f0 = ex2(M - ref);
-            L *= f0;
-            v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
-#pragma unroll
-            for (int i = 0; i < kJoin; ++i) {
-              const float f = ex2(ml[i].x - ref);
-              L = fmaf(ml[i].y, f, L);
-              v.x = fmaf(x[i].x, f, v.x);
-              v.y = fmaf(x[i].y, f, v.y);
-              v.z = fmaf(x[i].z, f, v.z);
-              v.w = fmaf(x[i].w, f, v.w);
-            }
-            M = top;
-          }
-          store(j, d, v, L);
-        }
+        join(tid, C::kThreads);
         if (tid == 0) st_relaxed_gpu(a.counters + unit, 0);
       }
     }
@@ -709,17 +768,18 @@ struct DecodeKernel {
   int threads;
 };
 template <bool BF16, int HD, int NB>
-DecodeKernel decode_kernel_of() {
+DecodeKernel decode_kernel_of(bool many = false) {
   using C = DecCfg<BF16, HD, NB>;
-  return DecodeKernel{&kv_decode_kernel<BF16, HD, NB>, C::kSmem, C::kThreads};
+  return DecodeKernel{many ? &kv_decode_kernel<BF16, HD, NB, NB == 1> : &kv_decode_kernel<BF16, HD, NB, false>, C::kSmem,
+                      C::kThreads};
 }
 template <bool BF16>
-DecodeKernel pick_decode(int Hd, int qc) {
+DecodeKernel pick_decode(int Hd, int qc, bool many) {
   switch (Hd) {
-    case 32: return qc == 16 ? decode_kernel_of<BF16, 32, 2>() : decode_kernel_of<BF16, 32, 1>();
-    case 64: return qc == 16 ? decode_kernel_of<BF16, 64, 2>() : decode_kernel_of<BF16, 64, 1>();
-    case 128: return qc == 16 ? decode_kernel_of<BF16, 128, 2>() : decode_kernel_of<BF16, 128, 1>();
-    default: return decode_kernel_of<BF16, 256, 1>();
+    case 32: return qc == 16 ? decode_kernel_of<BF16, 32, 2>() : decode_kernel_of<BF16, 32, 1>(many);
+    case 64: return qc == 16 ? decode_kernel_of<BF16, 64, 2>() : decode_kernel_of<BF16, 64, 1>(many);
+    case 128: return qc == 16 ? decode_kernel_of<BF16, 128, 2>() : decode_kernel_of<BF16, 128, 1>(many);
+    default: return decode_kernel_of<BF16, 256, 1>(many);
   }
 }
 
@@ -730,7 +790,8 @@ DecodeWs decode_ws(int B, int Tq, int Hq, int Hkv, int Hd) {
   const int nq = Hq / Hkv * Tq, qc = chunk_queries(nq, Hd), chunks = (nq + qc - 1) / qc;
   DecodeWs w;
   w.partials = 0;
-  w.counters = align16((size_t)2 * kMaxPagedCtas * partial_floats(std::min(nq, qc), Hd) * sizeof(float));
+  w.counters = align16((size_t)2 * (qc == 8 ? kMaxSolo : kMaxPagedCtas) * partial_floats(std::min(nq, qc), Hd) *
+                       sizeof(float));
   w.total = w.counters + align16((size_t)B * Hkv * chunks * sizeof(int32_t));
   return w;
 }
@@ -856,7 +917,8 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   const DecodeWs ws = decode_ws(B, Tq, Hq, Hkv, Hd);
   if (workspace_bytes < ws.total) return WSVD_ERR_WORKSPACE_TOO_SMALL;
   const int qc = chunk_queries((int)nq, Hd);
-  const DecodeKernel kern = dtype == WSVD_DTYPE_BF16 ? pick_decode<true>(Hd, qc) : pick_decode<false>(Hd, qc);
+  const bool many = (long long)B * Hkv * ((nq + qc - 1) / qc) >= kSoloUnits;
+  const DecodeKernel kern = dtype == WSVD_DTYPE_BF16 ? pick_decode<true>(Hd, qc, many) : pick_decode<false>(Hd, qc, many);
   KvDecodeArgs a{};
   a.Tq = Tq; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.nq = (int)nq; a.chunks = (int)((nq + qc - 1) / qc);
   a.seqs = PagedSeqs{B, Hkv * a.chunks, max_pages << shift, seq_lens};

@@ -20,24 +20,24 @@ struct PagedSeqs {
   }
 };
 
-// A unit's rows are cut into strips of TS rows, and counts as its strips plus
-// LEAD (what a segment costs beside its strips: queries, joins) when the shares
+// A unit's rows are cut into strips of TS rows, and counts as its strips plus a
+// lead (what a segment costs beside its strips: queries, joins) when the shares
 // of the workers (CTAs or warps) are cut, else a worker that meets many short
 // sequences would finish last.
-template <int TS, int LEAD>
+template <int TS>
 struct Strips {
   // A worker's share of one unit: strips [s, e) of unit u of sequence b (n
   // rows); none when the share ends within the lead.
   struct Segment {
-    int b, u, n, s, e;
+    int b, u, n, s, e, lead;
     int at, taken;   // where the share begins in the unit (lead included), and how much of the unit it takes
     long long left;  // of the worker's share from here on
     __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
     __device__ __forceinline__ void enter(int place) {
       at = place;
-      taken = (int)min((long long)(strips() + LEAD - at), left);
-      s = max(0, at - LEAD);
-      e = max(0, at + taken - LEAD);
+      taken = (int)min((long long)(strips() + lead - at), left);
+      s = max(0, at - lead);
+      e = max(0, at + taken - lead);
     }
     __device__ __forceinline__ bool next(const PagedSeqs& q) {
       left -= taken;
@@ -52,7 +52,7 @@ struct Strips {
     }
   };
 
-  static __device__ __forceinline__ int counted(int n) { return n > 0 ? (n + TS - 1) / TS + LEAD : 0; }
+  static __device__ __forceinline__ int strips_of(int n) { return (n + TS - 1) / TS; }
 
   long long total, base, extra, end;  // strips in all; per worker; workers with one more; this worker's end
   int workers;                        // workers that have a share
@@ -64,55 +64,76 @@ struct Strips {
   }
   // The workers that hold strips of the segment's unit: the first, and how many.
   __device__ __forceinline__ void holders(const Segment& g, int* first, int* count) const {
-    const long long u0 = end - g.left - g.at + LEAD;  // the unit's first strip in the whole order
+    const long long u0 = end - g.left - g.at + g.lead;  // the unit's first strip in the whole order
     *first = worker_of(u0);
     *count = worker_of(u0 + g.strips() - 1) - *first + 1;
   }
 
-  // Worker c's share (of `count` workers) and its first segment; false when it
-  // has none.  Every warp finds it for itself (all lanes take part).  `least`:
-  // strips a worker takes at least, so that a small problem is not cut too finely.
-  __device__ __forceinline__ bool deal(const PagedSeqs& q, int c, int count, int least, int32_t* err, Segment* seg) {
+  // How the strips are dealt: this worker of `count`, `least` strips a worker at
+  // least (so that a small problem is not cut too finely), a unit's lead.
+  struct Plan {
+    int me, count, least, lead;
+  };
+
+  // This worker's share and its first segment; false when it has none.  Every
+  // warp finds it for itself (all lanes take part).  plan(mean, live): the Plan
+  // for `live` sequences that have rows, whose units have `mean` strips on average.
+  template <class F>
+  __device__ __forceinline__ bool deal(const PagedSeqs& q, F plan, int32_t* err, Segment* seg) {
     const int lane = threadIdx.x & 31;
     const int per = (q.B + 31) / 32;
     const int b0 = min(q.B, lane * per), b1 = min(q.B, b0 + per);
     long long sum = 0;
+    int live = 0;
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-      const int raw = q.seq_lens[b];
-      if ((raw < 0 || raw > q.cap) && c == 0) set_err(err, WSVD_DEVERR_LEN_RANGE);
-      sum += counted(q.rows(b));
+      const int raw = q.seq_lens[b], n = raw < 0 || raw > q.cap ? 0 : raw;
+      if (n != raw && blockIdx.x == 0) set_err(err, WSVD_DEVERR_LEN_RANGE);
+      sum += strips_of(n);
+      live += n > 0;
     }
     long long incl = sum;
+    int lives = live;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int w = __shfl_up_sync(0xffffffffu, lives, o);
+      if (lane >= o) {
+        incl += v;
+        lives += w;
+      }
     }
-    const long long before = (incl - sum) * q.units;
-    total = __shfl_sync(0xffffffffu, incl, 31) * q.units;
-    const long long most = (total + least - 1) / least;
-    workers = (int)(most < count ? most : count);
-    if (c >= workers) return false;
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    const int all_live = __shfl_sync(0xffffffffu, lives, 31);
+    if (all_live == 0) return false;
+    const Plan p = plan(total < 0x80000000ll ? (int)((uint32_t)total / (uint32_t)all_live) : 0x7fffffff, all_live);
+    total = (total + (long long)all_live * p.lead) * q.units;
+    const long long most = (total + p.least - 1) / p.least;
+    workers = (int)(most < p.count ? most : p.count);
+    if (p.me >= workers) return false;
     base = (unsigned long long)total < 0x80000000ull ? (uint32_t)total / (uint32_t)workers : total / workers;
     extra = total - base * workers;
-    const long long begin = begin_of(c);
-    end = begin + base + (c < extra ? 1 : 0);
-    const bool mine = begin >= before && begin < before + sum * q.units;
+    const long long begin = begin_of(p.me);
+    end = begin + base + (p.me < extra ? 1 : 0);
+    const long long before = (incl - sum + (long long)(lives - live) * p.lead) * q.units;
+    const long long mine = (sum + (long long)live * p.lead) * q.units;
+    const bool here = begin >= before && begin < before + mine;
     long long rem = begin - before;
     int sb = b0;
-    if (mine)
+    if (here)
       for (;; ++sb) {
-        const long long ns = (long long)counted(q.rows(sb)) * q.units;
+        const int n = q.rows(sb);
+        const long long ns = n > 0 ? (long long)(strips_of(n) + p.lead) * q.units : 0;
         if (rem < ns) break;
         rem -= ns;
       }
-    const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
     seg->b = __shfl_sync(0xffffffffu, sb, src);
     rem = __shfl_sync(0xffffffffu, rem, src);
     seg->n = q.rows(seg->b);
     seg->left = end - begin;
-    const int unit = seg->strips() + LEAD;
+    seg->lead = p.lead;
+    const int unit = seg->strips() + p.lead;
     seg->u = (int)(rem / unit);
     seg->enter((int)(rem % unit));
     return true;

@@ -229,9 +229,12 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
   for (int b = blockIdx.x; b < seqs.B; b += gridDim.x)
     if (seqs.rows(b) == 0)
       for (int i = tid; i < H * Hd; i += C::kThreads) a.out[(size_t)b * H * Hd + i] = 0.f;
-  Strips<TS, C::kLead> share;
-  typename Strips<TS, C::kLead>::Segment seg;
-  if (!share.deal(seqs, me, min((int)gridDim.x * NW, kMaxDecodeCtas), 1, a.err, &seg)) return;
+  Strips<TS> share;
+  typename Strips<TS>::Segment seg;
+  const auto plan = [&](int, int) {
+    return typename Strips<TS>::Plan{me, min((int)gridDim.x * NW, kMaxDecodeCtas), 1, C::kLead};
+  };
+  if (!share.deal(seqs, plan, a.err, &seg)) return;
 
   // ---- the warp's copies: cursor `ld`; lane i holds the page of 16-row group i
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;

@@ -122,8 +122,9 @@ def test_workspace_sizes(lib):
     a16 = lambda v: (v + 15) // 16 * 16
     assert W.paged_kv_append_workspace_size(1) == 16 and W.paged_kv_append_workspace_size(9) == a16(36)
     assert W.paged_kv_append_workspace_size(-1) == 0
-    # two partials per CTA of at most 592, of O and (m, l) per query of a chunk; a counter per unit
-    size = lambda B, Hkv, nq, qc, Hd: (a16(2 * 592 * (min(nq, qc) * Hd + (2 * min(nq, qc) + 3) // 4 * 4) * 4)
+    # two partials per worker (592 CTAs, or 2048 warps with 8 queries a chunk), of O and (m, l) per query of
+    # a chunk; a counter per unit
+    size = lambda B, Hkv, nq, qc, Hd: (a16(2 * (2048 if qc == 8 else 592) * (min(nq, qc) * Hd + (2 * min(nq, qc) + 3) // 4 * 4) * 4)
                                        + a16(B * Hkv * math.ceil(nq / qc) * 4))
     assert W.paged_decode_workspace_size(3, 1, 32, 8, 128) == size(3, 8, 4, 8, 128)
     assert W.paged_decode_workspace_size(3, 4, 32, 4, 64) == size(3, 4, 32, 16, 64)
