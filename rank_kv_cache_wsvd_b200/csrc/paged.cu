@@ -292,11 +292,13 @@ constexpr int kLead = 24;
 
 // Up to 8 queries a head, many units and sequences of few strips: every warp is a
 // worker with segments of its own, nothing waits for a CTA, and most units end in
-// one warp's registers.  Measured with CTAs / warps as workers (us; 8 heads of
-// 128, 4 queries each): 256 x 128 rows 56.4 / 36.7, 64 x 1..300 rows 23.5 / 20.4, 64 x
-// 500 33.8 / 33.7, 32 x 1000 30.2 / 33.8; one sequence of 300 rows, whose few units
-// warps would have to join, 7.8 / 15.
-constexpr int kSoloStrips = 32, kSoloUnits = 512, kSoloLead = 4;
+// one warp's registers.  Measured with CTAs / warps as workers (us, head size 128):
+// 256 sequences x 128 rows of 8 heads, 4 queries each 56.4 / 36.5; 64 x 200 rows of 32
+// heads 68.4 / 42.9, 64 x 500 95.7 / 88.4, 32 x 1000 87.9 / 86.9; 8 heads with 4 queries,
+// 64 x 500 33.8 / 33.7, 256 x 500 99.7 / 96.6, 256 x 1000 168 / 172, 32 x 1000 30.2 / 33.8;
+// with 8 queries 64 x 300 28.4 / 30.0; one sequence of 300 rows, whose few units warps
+// would have to join, 7.8 / 15.
+constexpr int kSoloStrips = 40, kSoloUnits = 512, kSoloLead = 4;
 constexpr int kMaxSolo = 2048;  // workers that way at most; sizes the partials
 
 // MANY: many units, so that their sequences may be short (kSoloUnits); a kernel of

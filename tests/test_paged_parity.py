@@ -447,6 +447,39 @@ def test_decode_thousands_of_short_sequences():
     assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("Hd,G,Tq", [(32, 8, 1), (64, 1, 1), (64, 2, 3), (128, 7, 1), (256, 4, 2)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_decode_many_short_sequences(Hd, G, Tq, dtype):
+    """Over 512 units of few strips, where every warp works for itself: whole units,
+    cut ones, sequences without rows, bad lengths and bad pages among them; the
+    same bits again, also when long sequences (CTAs as workers) used the
+    workspace in between."""
+    B, Hkv = 130, 4
+    lens = [(b * 37) % 260 if b % 9 else 0 for b in range(B)]
+    lens[5] = 3000
+    kp, vp, table = _cache(lens, Hkv, Hd, 32, dtype, seed=Hd + G)
+    q = randn((B, Tq, Hkv * G, Hd), dtype, 4)
+    ws = W.workspace(W.paged_decode_workspace_size(B, Tq, Hkv * G, Hkv, Hd))
+    out, err = _decode(q, kp, vp, table, lens, workspace_buf=ws)
+    assert err == 0
+    some = list(range(0, 24)) + [60, 99, 129]
+    _check_decode(out[some], q[some], kp.nan_to_num(0), vp.nan_to_num(0), table[some], [lens[b] for b in some],
+                  what=f"Hd{Hd} G{G} Tq{Tq}")
+    assert (out[[b for b in range(B) if lens[b] == 0]] == 0).all() and torch.isfinite(out).all()
+    long = [3000] * 4 + [0] * (B - 4)
+    big, err = _decode(q, kp, vp, np.repeat(table[5:6], B, 0), long, workspace_buf=ws)
+    assert err == 0
+    again, _ = _decode(q, kp, vp, table, lens, workspace_buf=ws)
+    assert torch.equal(again, out)
+    broken, odd = table.copy(), list(lens)
+    broken[10, 1], odd[11] = kp.shape[0], -3
+    bad, err = _decode(q, kp, vp, broken, odd)
+    rest = [b for b in range(B) if b not in (10, 11)]
+    assert err == W.DEVERR_PAGE_RANGE | 1 and (bad[11] == 0).all()
+    _check_decode(bad[rest[:20]], q[rest[:20]], kp.nan_to_num(0), vp.nan_to_num(0), table[rest[:20]],
+                  [lens[b] for b in rest[:20]], what="beside bad ones")
+
+
 def test_paged_decode_matches_the_contiguous_one():
     """The same rows in pages and in the dense cache: both within the allowance
     of the float64 value."""
