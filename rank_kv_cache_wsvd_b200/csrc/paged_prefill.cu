@@ -21,7 +21,9 @@
 //              rounding to nearest (the tensor cores' own sums do not).
 // Where there are few tiles a cluster of up to 8 CTAs splits E for one tile; the
 // ranks' sums are read through the cluster's shared memory in rank order, each
-// rank quantising its share of the tokens.
+// rank quantising its share of the tokens.  Bound by the operand tiles' L2 bytes:
+// 576 tokens, 32 heads of r 32, E 4096 33 us (221 MB of tiles; the products alone,
+// hi and lo, 11.7), 16 tokens 15.4.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -127,23 +129,24 @@ __global__ void __launch_bounds__(512) block_rotate_kernel(const uint16_t* x, in
 // ------------------------------------------------------------------ 2. GEMM + quantise
 constexpr int kTokens = 64, kBK = 64;
 
-// TG: groups of 64 tokens a tile, which share its weights.
-template <int R, int BN_, int TG_>
+// Tiles of 256 columns have two epilogue threads a row, 128 columns each.
+template <int R, int BN_>
 struct BlockCfg {
-  static constexpr int BN = BN_, TG = TG_;
-  static constexpr int kRows = 128 * TG;                          // operand rows = epilogue threads
-  static constexpr int kThreads = kRows + 64;
+  static constexpr int BN = BN_;
+  static constexpr int CG = BN == 256 ? 2 : 1, COLS = BN / CG;   // column groups; columns a thread sums
+  static constexpr int kEpi = 128 * CG;                           // epilogue threads
+  static constexpr int kThreads = kEpi + 64;
   static constexpr int NG = R <= 64 ? R : 64;                    // columns per weight box
   static constexpr int SW = NG == 16 ? 6 : (NG == 32 ? 4 : 2);   // descriptor swizzle: 32 / 64 / 128 bytes
   static constexpr int HALF = kTokens * kBK * 2;                  // hi (or lo) rows of a stage
-  static constexpr int WOFF = 2 * HALF * TG;                      // weights behind the token rows
-  static constexpr int STAGE = WOFF + kBK * BN * 2;
-  static constexpr int S = TG == 1 ? 6 : 4;
-  static constexpr int NH = 512 / (BN * TG);                      // accumulators: all 512 columns
+  static constexpr int STAGE = 2 * HALF + kBK * BN * 2;
+  static constexpr int S = STAGE > 32768 ? 4 : 6;
+  static constexpr int NH = 512 / BN;                             // accumulators: all 512 columns
   static constexpr int PITCH = BN + 4;                            // floats per row of the sums
   static constexpr int SMEM = S * STAGE + 1024 + 256;
   static_assert(R <= BN && STAGE % 1024 == 0, "whole heads; stages keep the swizzle atoms' alignment");
-  static_assert((TG == 1 ? 3 * kTokens : kRows) * PITCH * 4 <= S * STAGE, "the sums reuse the ring");
+  static_assert((2 * kTokens + kTokens / 2) * PITCH * 4 <= S * STAGE,
+                "the operand rows' sums and a rank's share of the tokens reuse the ring");
 };
 
 struct BlockArgs {
@@ -177,14 +180,14 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int 
 }
 
 // grid (token tiles x ranks, column tiles of K then V)
-template <int R, int BN_, int TG_>
-__global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
+template <int R, int BN_>
+__global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tm_xhi, const __grid_constant__ CUtensorMap tm_xlo,
                       const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
                       const BlockArgs a, const PagedRows place) {
-  using C = BlockCfg<R, BN_, TG_>;
-  constexpr int BN = C::BN, NG = C::NG, S = C::S, NH = C::NH, TG = C::TG, kThreads = C::kThreads;
-  constexpr int kProducer = C::kRows / 32, kIssuer = kProducer + 1;  // warps
+  using C = BlockCfg<R, BN_>;
+  constexpr int BN = C::BN, NG = C::NG, S = C::S, NH = C::NH, kThreads = C::kThreads;
+  constexpr int kProducer = C::kEpi / 32, kIssuer = kProducer + 1;  // warps
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms need 1024-byte alignment
@@ -192,12 +195,12 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::STAGE);
   uint64_t* empty = full + S;
   uint64_t* hfull = empty + S;   // [NH] a k-tile's sums are in tensor memory
-  uint64_t* hfree = hfull + NH;  // [NH] they have been read (an arrival per row)
+  uint64_t* hfree = hfull + NH;  // [NH] they have been read (an arrival per thread)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(hfree + NH);
-  __shared__ int sm_pos[kTokens * TG], sm_why[kTokens * TG];  // of the tile's tokens: first row of its block, refusal
+  __shared__ int sm_pos[kTokens], sm_why[kTokens];  // of the tile's tokens: first row of its block, refusal
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int ranks = TG == 1 ? a.ranks : 1, rank = (int)blockIdx.x % ranks;
-  const int m0 = (int)blockIdx.x / ranks * (kTokens * TG);
+  const int ranks = a.ranks, rank = (int)blockIdx.x % ranks;
+  const int m0 = (int)blockIdx.x / ranks * kTokens;
   const int side = (int)gridDim.y / 2, kv = (int)blockIdx.y >= side, nl = ((int)blockIdx.y - kv * side) * BN;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     }
     for (int i = 0; i < NH; ++i) {
       mbar_init(&hfull[i], 1);
-      mbar_init(&hfree[i], C::kRows);
+      mbar_init(&hfree[i], C::kEpi);
     }
     fence_mbar_init();
   }
@@ -239,15 +242,12 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
 #pragma unroll
       for (int g = 0; g < BN / NG; ++g) {
         const int col = nl + g * NG;  // heads past the last are filled with zeros
-        tma_3d(st + C::WOFF + g * (kBK * NG * 2), wmap, col % R, k0, col / R, &full[s]);
+        tma_3d(st + 2 * C::HALF + g * (kBK * NG * 2), wmap, col % R, k0, col / R, &full[s]);
       }
       if (!waited) griddep_wait();
       waited = true;
-#pragma unroll
-      for (int g = 0; g < TG; ++g) {  // tokens past the last are filled with zeros
-        tma_2d(st + 2 * g * C::HALF, &tm_xhi, k0, m0 + g * kTokens, &full[s]);
-        tma_2d(st + (2 * g + 1) * C::HALF, &tm_xlo, k0, m0 + g * kTokens, &full[s]);
-      }
+      tma_2d(st, &tm_xhi, k0, m0, &full[s]);  // tokens past the last are filled with zeros
+      tma_2d(st + C::HALF, &tm_xlo, k0, m0, &full[s]);
     }
     for (int kt = std::max(0, KT - S); kt < KT; ++kt) wait(&full[kt % S], (uint32_t)((kt / S) & 1));
     __syncwarp();
@@ -259,13 +259,11 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
       if (kt >= NH) wait(&hfree[hb], (uint32_t)(((kt / NH) - 1) & 1));
       __syncwarp();
       tc05::fence_after_sync();
-      const uint32_t st = base + (uint32_t)(s * C::STAGE), d = tmem + (uint32_t)(hb * BN * TG);
+      const uint32_t st = base + (uint32_t)(s * C::STAGE), d = tmem + (uint32_t)(hb * BN);
 #pragma unroll
       for (int kk = 0; kk < kBK / 16; ++kk)
-#pragma unroll
-        for (int g = 0; g < TG; ++g)
-          tc05::mma_f16_warp(d + (uint32_t)(g * BN), tc05::smem_desc_sw(st + 2 * g * C::HALF + kk * 32, 16, 1024, 2),
-                             tc05::smem_desc_sw(st + C::WOFF + kk * 32 * NG, 128 * NG, 16 * NG, C::SW), idesc, kk > 0);
+        tc05::mma_f16_warp(d, tc05::smem_desc_sw(st + kk * 32, 16, 1024, 2),
+                           tc05::smem_desc_sw(st + 2 * C::HALF + kk * 32 * NG, 128 * NG, 16 * NG, C::SW), idesc, kk > 0);
       tc05::commit_warp(&empty[s]);
       tc05::commit_warp(&hfull[hb]);
     }
@@ -273,26 +271,28 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     for (int kt = std::max(0, KT - NH); kt < KT; ++kt) wait(&hfull[kt % NH], (uint32_t)((kt / NH) & 1));
     __syncwarp();
   } else {  // ---------------------------------------------------------------- thread = operand row
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp >> 2) * BN);
-    const int token = (tid >> 7) * kTokens + (tid & (kTokens - 1)), m = m0 + token;
-    if ((tid & 127) < kTokens && m < a.M) {  // while the first tiles arrive
+    constexpr int COLS = C::COLS;
+    const int col0 = (tid >> 7) * COLS;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)col0;
+    const int token = tid & (kTokens - 1), m = m0 + token;
+    if (tid < kTokens && m < a.M) {  // while the first tiles arrive
       const int b = m / a.T, pos = ld_relaxed_gpu(a.seq_lens + b);
       sm_pos[token] = pos;
       sm_why[token] = place.refused(b, pos, a.T, a.cap);
     }
     __syncwarp();
-    float tot[BN];
+    float tot[COLS];
 #pragma unroll
-    for (int c = 0; c < BN; ++c) tot[c] = 0.f;
+    for (int c = 0; c < COLS; ++c) tot[c] = 0.f;
     for (int kt = 0; kt < KT; ++kt) {
       const int hb = kt % NH;
       wait(&hfull[hb], (uint32_t)((kt / NH) & 1));
       tc05::fence_after_sync();
 #pragma unroll
-      for (int c0 = 0; c0 < BN; c0 += 64) {  // two loads in flight per wait
+      for (int c0 = 0; c0 < COLS; c0 += 64) {  // two loads in flight per wait
         uint32_t va[32], vb[32];
-        tc05::ld32(lane_base + (uint32_t)(hb * BN * TG + c0), va);
-        tc05::ld32(lane_base + (uint32_t)(hb * BN * TG + c0 + 32), vb);
+        tc05::ld32(lane_base + (uint32_t)(hb * BN + c0), va);
+        tc05::ld32(lane_base + (uint32_t)(hb * BN + c0 + 32), vb);
         tc05::wait_ld();
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
@@ -305,19 +305,19 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     }
     griddep_wait();  // 1 / p comes from the rotation grid
     const float ip = m < a.M ? a.inv_p[m] : 0.f;
-    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + (size_t)tid * C::PITCH);
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) +
+                                            (size_t)(tid & 127) * C::PITCH + col0);
 #pragma unroll
-    for (int c = 0; c < BN; c += 4)
+    for (int c = 0; c < COLS; c += 4)
       dst[c / 4] = make_float4(tot[c] * ip, tot[c + 1] * ip, tot[c + 2] * ip, tot[c + 3] * ip);
   }
 
   // ---- the rank's share of the tokens: hi and lo of all ranks, in order
   cg::cluster_group cluster = cg::this_cluster();
-  float* part = reinterpret_cast<float*>(smem);  // per group [hi 64, lo 64][PITCH]
+  float* part = reinterpret_cast<float*>(smem);  // [hi 64, lo 64][PITCH]
   // The joined tokens [PITCH]: behind the parts that other ranks read, else over the hi rows.
   float* sums = ranks > 1 ? part + 2 * kTokens * C::PITCH : part;
-  const int r0 = kTokens * rank / ranks, rows = ranks > 1 ? kTokens * (rank + 1) / ranks - r0 : kTokens * TG;
-  auto at_row = [&](int row) { return (size_t)(ranks > 1 ? row : (row >> 6) * 128 + (row & 63)) * C::PITCH; };
+  const int r0 = kTokens * rank / ranks, rows = kTokens * (rank + 1) / ranks - r0;
   if (ranks > 1) cluster.sync();
   else __syncthreads();
   for (int i = tid; i < rows * (BN / 4); i += kThreads) {
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     if (m0 + r0 + row >= a.M) break;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (ranks == 1) {
-      const float* p = part + at_row(row) + c;
+      const float* p = part + (size_t)row * C::PITCH + c;
       const float4 x = *reinterpret_cast<const float4*>(p);
       const float4 y = *reinterpret_cast<const float4*>(p + (size_t)kTokens * C::PITCH);
       v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
@@ -345,22 +345,22 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
           v = make_float4(v.x + (x[q].x + y[q].x), v.y + (x[q].y + y[q].y), v.z + (x[q].z + y[q].z),
                           v.w + (x[q].w + y[q].w));
     }
-    *reinterpret_cast<float4*>(sums + at_row(row) + c) = v;
+    *reinterpret_cast<float4*>(sums + (size_t)row * C::PITCH + c) = v;
   }
   if (ranks > 1) cluster.sync();  // the ranks' sums have been read: a rank may leave
   else __syncthreads();
 
-  // ---- quantise: LPU threads to a (token, head) row, COLS of its columns each
-  constexpr int HEADS = BN / R, LPU = R > 32 ? R / 32 : 1, COLS = R / LPU;
+  // ---- quantise: LPU threads to a (token, head) row, QCOLS of its columns each
+  constexpr int HEADS = BN / R, LPU = R > 32 ? R / 32 : 1, QCOLS = R / LPU;
   const int Q = a.bits == 8 ? 127 : 7, RB = R * a.bits / 8;
   const int units = rows * HEADS * LPU;
   for (int u = tid; u < (units + 31) / 32 * 32; u += kThreads) {  // whole warps: the maximum crosses lanes
     const int row = u / (HEADS * LPU), hh = u / LPU % HEADS, sub = u % LPU, m = m0 + r0 + row, h = nl / R + hh;
     const bool real = u < units && m < a.M && h < a.H;
-    const float4* src = reinterpret_cast<const float4*>(sums + at_row(u < units ? row : 0) + hh * R + sub * COLS);
-    float v[COLS], amax = 0.f;
+    const float4* src = reinterpret_cast<const float4*>(sums + (size_t)(u < units ? row : 0) * C::PITCH + hh * R + sub * QCOLS);
+    float v[QCOLS], amax = 0.f;
 #pragma unroll
-    for (int c = 0; c < COLS / 4; ++c) {
+    for (int c = 0; c < QCOLS / 4; ++c) {
       const float4 x = src[c];
       v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
       amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
@@ -377,10 +377,10 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
     const float sc = __half2float(sh);
     const size_t at = place.row(b, h, a.H, pos + t, a.cap);
     auto code = [&](int j) { return sc > 0.f ? max(-Q, min(Q, __float2int_rn(__fdiv_rn(v[j], sc)))) : 0; };
-    uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.lat_v : a.lat_k) + at * RB + sub * (COLS * a.bits / 8));
+    uint32_t* dst = reinterpret_cast<uint32_t*>((kv ? a.lat_v : a.lat_k) + at * RB + sub * (QCOLS * a.bits / 8));
     if (a.bits == 8) {
 #pragma unroll
-      for (int w = 0; w < COLS / 4; ++w) {
+      for (int w = 0; w < QCOLS / 4; ++w) {
         uint32_t x = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) x |= ((uint32_t)code(4 * w + k) & 0xFFu) << (8 * k);
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TG_>::kThreads, 1)
       }
     } else {
 #pragma unroll
-      for (int w = 0; w < COLS / 8; ++w) {
+      for (int w = 0; w < QCOLS / 8; ++w) {
         uint32_t x = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) x |= ((uint32_t)code(8 * w + k) & 0xFu) << (4 * k);
@@ -492,22 +492,22 @@ int resident_clusters(const void* kern, int threads, size_t smem, int c) {
   return known[key] = n;
 }
 
-template <int R, int BN, int TG>
+template <int R, int BN>
 cudaError_t launch_tiles(BlockArgs a, const __half* xhi, const __half* xlo, int E, const void* A_k, const void* A_v,
                          const PagedRows& place, cudaStream_t s) {
-  using C = BlockCfg<R, BN, TG>;
-  auto kern = block_gemm_kernel<R, BN, TG>;
+  using C = BlockCfg<R, BN>;
+  auto kern = block_gemm_kernel<R, BN>;
   const void* fn = reinterpret_cast<const void*>(kern);
   CUtensorMap mh, ml, mk, mv;
   if (!token_map(&mh, xhi, a.M, E) || !token_map(&ml, xlo, a.M, E) || !weight_map(&mk, A_k, a.H, E, R, C::NG) ||
       !weight_map(&mv, A_v, a.H, E, R, C::NG))
     return cudaErrorInvalidValue;
   if (resident_clusters(fn, C::kThreads, C::SMEM, 1) < 1) return cudaErrorInvalidConfiguration;
-  const int mt = (a.M + kTokens * TG - 1) / (kTokens * TG), nt = 2 * ((a.H * R + BN - 1) / BN);
+  const int mt = (a.M + kTokens - 1) / kTokens, nt = 2 * ((a.H * R + BN - 1) / BN);
   a.KT = E / kBK;
   // The most ranks whose clusters all run at once, at least two k-tiles each.
   a.ranks = 1;
-  for (int c = 8; TG == 1 && c > 1 && a.ranks == 1; c >>= 1)
+  for (int c = 8; c > 1 && a.ranks == 1; c >>= 1)
     if (2 * c <= a.KT && (long long)mt * nt <= resident_clusters(fn, C::kThreads, C::SMEM, c)) a.ranks = c;
   a.ctas = mt * a.ranks * nt;
   cudaLaunchAttribute attr[2];
@@ -527,17 +527,24 @@ cudaError_t launch_tiles(BlockArgs a, const __half* xhi, const __half* xlo, int 
   return cudaLaunchKernelEx(&cfg, kern, mh, ml, mk, mv, a, place);
 }
 
-// Tiles of 64 tokens where they fit one wave of CTAs; past that tiles of 128,
-// whose weights are fetched once for twice the tokens (a tile of 128 takes about
-// 1.75 times one of 64), unless they leave the last wave emptier.
-template <int R, int BN>
+// Which tile.  The operand tiles come from L2 and bound the kernel once the CTAs
+// fill the device: 64 x 128 fetches 32 KB a k-tile, 64 x 256 48 KB for twice the
+// columns.  With half a wave of tiles or fewer the narrow ones keep more SMs at
+// work.  Measured, 128 / 256 columns in us (32 heads, E 4096): r 32, 16 tokens 15.4 /
+// 16.6, 128 18.2 / 22.3, 320 33.8 / 29.5, 576 36.6 / 32.8, 1728 102 / 95; r 64, 128
+// 23.1 / 23.9, 256 34.7 / 28.9, 576 68.1 / 44.9, 1728 195 / 127; r 128, 128 34.5 / 29.8;
+// r 16, 576 30.0 / 29.8, 1728 79.5 / 69.  (Tiles of 128 tokens x 128 columns took 50.5
+// for 576 tokens of r 32, 178 for 1728 of r 64; they led only for r 16 with E 2048,
+// 75.7 against 88.8 for 4096 tokens.)  Columns past a side's last head are idle: at most a quarter of them.
+template <int R>
 cudaError_t launch_block(const BlockArgs& a, const __half* xhi, const __half* xlo, int E, const void* A_k,
                          const void* A_v, const PagedRows& place, cudaStream_t s) {
-  const int nt = 2 * ((a.H * R + BN - 1) / BN), sms = 148;
-  const int waves1 = ((a.M + 63) / 64 * nt + sms - 1) / sms, waves2 = ((a.M + 127) / 128 * nt + sms - 1) / sms;
-  if (BN == 128 && waves1 > 1 && 7 * waves2 <= 4 * waves1)
-    return launch_tiles<R, BN, BN == 128 ? 2 : 1>(a, xhi, xlo, E, A_k, A_v, place, s);
-  return launch_tiles<R, BN, 1>(a, xhi, xlo, E, A_k, A_v, place, s);
+  const int hr = a.H * R, sms = 148, mt = (a.M + kTokens - 1) / kTokens;
+  if ((long long)mt * 2 * ((hr + 127) / 128) > sms / 2 && 4 * ((hr + 255) / 256 * 256) <= 5 * hr)
+    return launch_tiles<R, 256>(a, xhi, xlo, E, A_k, A_v, place, s);
+  if constexpr (R <= 64)
+    if (hr <= 64) return launch_tiles<R, 64>(a, xhi, xlo, E, A_k, A_v, place, s);
+  return launch_tiles<R, 128>(a, xhi, xlo, E, A_k, A_v, place, s);
 }
 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
@@ -575,18 +582,11 @@ cudaError_t launch_paged_block(const AppendArgs& p, int T, const PagedRows& plac
   a.inv_p = inv; a.seq_lens = p.seq_lens;
   a.lat_k = p.lat_k; a.lat_v = p.lat_v; a.scale_k = p.scale_k; a.scale_v = p.scale_v;
   a.counter = p.counter; a.err = p.err;
-  const bool wide = p.H * p.r >= 128;
   switch (p.r) {
-    case 16:
-      return wide ? launch_block<16, 128>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s)
-                  : launch_block<16, 64>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
-    case 32:
-      return wide ? launch_block<32, 128>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s)
-                  : launch_block<32, 64>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
-    case 64:
-      return wide ? launch_block<64, 128>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s)
-                  : launch_block<64, 64>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
-    case 128: return launch_block<128, 128>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
+    case 16: return launch_block<16>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
+    case 32: return launch_block<32>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
+    case 64: return launch_block<64>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
+    case 128: return launch_block<128>(a, xhi, xlo, p.E, p.Ak, p.Av, place, s);
     default: return cudaErrorInvalidValue;
   }
 }

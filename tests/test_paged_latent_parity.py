@@ -275,7 +275,8 @@ def _check_rows(lk, lv, sk, sv, table, lens, x, Ak, Av, bits, page, blk):
 @pytest.mark.parametrize("B,T,H,E,blk", [(1, 1, 4, 256, 128), (5, 1, 3, 512, 64), (20, 1, 4, 256, 128), (2, 1, 8, 1024, 256),
                                          (3, 37, 4, 256, 128), (2, 130, 3, 192, 1), (1, 200, 16, 1024, 128),
                                          (40, 1, 16, 2048, 1024), (1, 70, 1, 64, 16), (9, 1, 2, 272, 16),
-                                         (2, 201, 16, 128, 64), (1, 700, 16, 128, 32)])
+                                         (2, 201, 16, 128, 64), (1, 700, 16, 128, 32), (1, 1300, 3, 64, 64),
+                                         (1, 300, 32, 256, 128)])
 def test_latent_append_writes_its_rows_and_no_others(bits, r, page, B, T, H, E, blk):
     """Both paths (the GEMV; the tensor-core GEMM, whole and with E split over a
     cluster, tiles that run past the last head) against the oracle; one token as
