@@ -9,11 +9,12 @@
 //      with the quantiser in its epilogue; the last CTA to finish advances the
 //      lengths.
 //
-// A tile is 64 tokens x BN columns (whole heads of K or of V).  The hi rows of
-// its tokens and their lo rows stand one above the other in one 128-row operand,
-// so one MMA makes both products and reads the weights once for the two (the
-// contiguous prefill issues two, over 128 tokens each):
-//   warp 4     TMA producer: per 64-wide k-tile hi [64 x 64], lo [64 x 64] and
+// A tile is TOK tokens x BN columns (whole heads of K or of V).  64 tokens: the hi rows
+// and the lo rows stand one above the other in one 128-row operand, so one MMA makes
+// both products.  128 tokens, where there are many: the products are made in turn, lo
+// then hi, into one accumulator, over the same weights.  Warps of a tile of 128 columns
+// (of 256: warps 0-7 sum, two threads a row, then the producer and the issuer):
+//   warp 4     TMA producer: per 64-wide k-tile hi [TOK x 64], lo [TOK x 64] and
 //              the weights [64 x BN], a ring of mbarrier stages;
 //   warp 5     allocates tensor memory and issues four k16 MMAs per k-tile into a
 //              fresh accumulator of NH;
@@ -21,9 +22,10 @@
 //              rounding to nearest (the tensor cores' own sums do not).
 // Where there are few tiles a cluster of up to 8 CTAs splits E for one tile; the
 // ranks' sums are read through the cluster's shared memory in rank order, each
-// rank quantising its share of the tokens.  Bound by the operand tiles' L2 bytes:
-// 576 tokens, 32 heads of r 32, E 4096 33 us (221 MB of tiles; the products alone,
-// hi and lo, 11.7), 16 tokens 15.4.
+// rank quantising its share of the tokens.  Bound by the operand tiles' way from L2
+// (75 to 90 GB/s a SM whatever the tile): 32 heads of r 32, E 4096, both kernels:
+// 576 tokens 30.7 us (221 MB of tiles; the products alone, hi and lo, 11.7), 4096 tokens
+// 160 (1.0 GB; 83), 16 tokens 14.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -135,26 +137,28 @@ __global__ void __launch_bounds__(512) block_rotate_kernel(const uint16_t* x, in
 }
 
 // ------------------------------------------------------------------ 2. GEMM + quantise
-constexpr int kTokens = 64, kBK = 64;
+constexpr int kBK = 64, kSMs = 148;
 
-// Tiles of 256 columns have two epilogue threads a row, 128 columns each.
-template <int R, int BN_>
+// TOK tokens a tile, 64 (hi above lo) or 128 (hi and lo products in turn).  Tiles of 256 columns have two epilogue threads a row, 128 columns each.
+template <int R, int BN_, int TOK_>
 struct BlockCfg {
-  static constexpr int BN = BN_;
+  static constexpr int BN = BN_, TOK = TOK_;
   static constexpr int CG = BN == 256 ? 2 : 1, COLS = BN / CG;   // column groups; columns a thread sums
   static constexpr int kEpi = 128 * CG;                           // epilogue threads
   static constexpr int kThreads = kEpi + 64;
   static constexpr int NG = R <= 64 ? R : 64;                    // columns per weight box
   static constexpr int SW = NG == 16 ? 6 : (NG == 32 ? 4 : 2);   // descriptor swizzle: 32 / 64 / 128 bytes
-  static constexpr int HALF = kTokens * kBK * 2;                  // hi (or lo) rows of a stage
+  static constexpr int HALF = TOK * kBK * 2;                      // hi (or lo) rows of a stage
   static constexpr int STAGE = 2 * HALF + kBK * BN * 2;
-  static constexpr int S = STAGE > 32768 ? 4 : 6;
+  static constexpr int S = 196608 / STAGE < 6 ? 196608 / STAGE : 6;
   static constexpr int NH = 512 / BN;                             // accumulators: all 512 columns
   static constexpr int PITCH = BN + 4;                            // floats per row of the sums
-  static constexpr int SMEM = S * STAGE + 1024 + 256;
+  // The sums reuse the ring: 128 operand rows, and behind them a rank's share of the tokens.
+  static constexpr int SUMS = (128 + TOK / 2) * PITCH * 4;
+  static constexpr int RING = SUMS > S * STAGE ? SUMS : S * STAGE;
+  static constexpr int SMEM = RING + 1024 + 256;
   static_assert(R <= BN && STAGE % 1024 == 0, "whole heads; stages keep the swizzle atoms' alignment");
-  static_assert((2 * kTokens + kTokens / 2) * PITCH * 4 <= S * STAGE,
-                "the operand rows' sums and a rank's share of the tokens reuse the ring");
+  static_assert(TOK == 64 || TOK == 128, "operand rows");
 };
 
 struct BlockArgs {
@@ -187,28 +191,37 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int 
       : "memory");
 }
 
+// a += x, b += y, rounding to nearest.
+__device__ __forceinline__ void add2(float& a, float& b, uint32_t x, uint32_t y) {
+  asm("{\n\t.reg .b64 s, t;\n\t"
+      "mov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, t;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(x), "r"(y));
+}
+
 // grid (token tiles x ranks, column tiles of K then V)
-template <int R, int BN_>
-__global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
+template <int R, int BN_, int TOK_>
+__global__ void __launch_bounds__(BlockCfg<R, BN_, TOK_>::kThreads, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tm_xhi, const __grid_constant__ CUtensorMap tm_xlo,
                       const __grid_constant__ CUtensorMap tm_wk, const __grid_constant__ CUtensorMap tm_wv,
                       const BlockArgs a, const PagedRows place) {
-  using C = BlockCfg<R, BN_>;
-  constexpr int BN = C::BN, NG = C::NG, S = C::S, NH = C::NH, kThreads = C::kThreads;
+  using C = BlockCfg<R, BN_, TOK_>;
+  constexpr int BN = C::BN, TOK = C::TOK, NG = C::NG, S = C::S, NH = C::NH, kThreads = C::kThreads;
   constexpr int kProducer = C::kEpi / 32, kIssuer = kProducer + 1;  // warps
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms need 1024-byte alignment
   uint8_t* smem = smem_raw + (base - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING);
   uint64_t* empty = full + S;
   uint64_t* hfull = empty + S;   // [NH] a k-tile's sums are in tensor memory
-  uint64_t* hfree = hfull + NH;  // [NH] they have been read (an arrival per thread)
+  uint64_t* hfree = hfull + NH;  // [NH] they have been read (an arrival per warp)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(hfree + NH);
-  __shared__ int sm_pos[kTokens], sm_why[kTokens];  // of the tile's tokens: first row of its block, refusal
+  __shared__ int sm_pos[TOK], sm_why[TOK];  // of the tile's tokens: first row of its block, refusal
   const int tid = threadIdx.x, warp = tid >> 5;
   const int ranks = a.ranks, rank = (int)blockIdx.x % ranks;
-  const int m0 = (int)blockIdx.x / ranks * kTokens;
+  const int m0 = (int)blockIdx.x / ranks * TOK;
   const int side = (int)gridDim.y / 2, kv = (int)blockIdx.y >= side, nl = ((int)blockIdx.y - kv * side) * BN;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
     }
     for (int i = 0; i < NH; ++i) {
       mbar_init(&hfull[i], 1);
-      mbar_init(&hfree[i], C::kEpi);
+      mbar_init(&hfree[i], C::kEpi / 32);
     }
     fence_mbar_init();
   }
@@ -260,7 +273,7 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
     for (int kt = std::max(0, KT - S); kt < KT; ++kt) wait(&full[kt % S], (uint32_t)((kt / S) & 1));
     __syncwarp();
   } else if (warp == kIssuer) {  // ----------------------------------------- MMA issuer
-    constexpr uint32_t idesc = tc05::instr_desc(1, 0, 0, 0, 1, 2 * kTokens, BN);
+    constexpr uint32_t idesc = tc05::instr_desc(1, 0, 0, 0, 1, 128, BN);
     for (int kt = 0; kt < KT; ++kt) {
       const int s = kt % S, hb = kt % NH;
       wait(&full[s], (uint32_t)((kt / S) & 1));
@@ -269,9 +282,12 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
       tc05::fence_after_sync();
       const uint32_t st = base + (uint32_t)(s * C::STAGE), d = tmem + (uint32_t)(hb * BN);
 #pragma unroll
-      for (int kk = 0; kk < kBK / 16; ++kk)
-        tc05::mma_f16_warp(d, tc05::smem_desc_sw(st + kk * 32, 16, 1024, 2),
-                           tc05::smem_desc_sw(st + 2 * C::HALF + kk * 32 * NG, 128 * NG, 16 * NG, C::SW), idesc, kk > 0);
+      for (int op = TOK == 64 ? 0 : 1; op >= 0; --op)  // lo first: the sum grows last
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          tc05::mma_f16_warp(d, tc05::smem_desc_sw(st + op * C::HALF + kk * 32, 16, 1024, 2),
+                             tc05::smem_desc_sw(st + 2 * C::HALF + kk * 32 * NG, 128 * NG, 16 * NG, C::SW), idesc,
+                             kk > 0 || (TOK == 128 && op == 0));
       tc05::commit_warp(&empty[s]);
       tc05::commit_warp(&hfull[hb]);
     }
@@ -282,8 +298,8 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
     constexpr int COLS = C::COLS;
     const int col0 = (tid >> 7) * COLS;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)col0;
-    const int token = tid & (kTokens - 1), m = m0 + token;
-    if (tid < kTokens && m < a.M) {  // while the first tiles arrive
+    const int token = tid & (TOK - 1), m = m0 + token;
+    if (tid < TOK && m < a.M) {  // while the first tiles arrive
       const int b = m / a.T, pos = ld_relaxed_gpu(a.seq_lens + b);
       sm_pos[token] = pos;
       sm_why[token] = place.refused(b, pos, a.T, a.cap);
@@ -303,13 +319,14 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
         tc05::ld32(lane_base + (uint32_t)(hb * BN + c0 + 32), vb);
         tc05::wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          tot[c0 + c] = __fadd_rn(tot[c0 + c], __uint_as_float(va[c]));
-          tot[c0 + 32 + c] = __fadd_rn(tot[c0 + 32 + c], __uint_as_float(vb[c]));
+        for (int c = 0; c < 32; c += 2) {
+          add2(tot[c0 + c], tot[c0 + c + 1], va[c], va[c + 1]);
+          add2(tot[c0 + 32 + c], tot[c0 + 33 + c], vb[c], vb[c + 1]);
         }
       }
       tc05::fence_before_sync();
-      mbar_arrive(&hfree[hb]);
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(&hfree[hb]);
     }
     griddep_wait();  // 1 / p comes from the rotation grid
     const float ip = m < a.M ? a.inv_p[m] : 0.f;
@@ -322,37 +339,30 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_>::kThreads, 1)
 
   // ---- the rank's share of the tokens: hi and lo of all ranks, in order
   cg::cluster_group cluster = cg::this_cluster();
-  float* part = reinterpret_cast<float*>(smem);  // [hi 64, lo 64][PITCH]
+  float* part = reinterpret_cast<float*>(smem);  // [hi 64, lo 64] or [128][PITCH]
   // The joined tokens [PITCH]: behind the parts that other ranks read, else over the hi rows.
-  float* sums = ranks > 1 ? part + 2 * kTokens * C::PITCH : part;
-  const int r0 = kTokens * rank / ranks, rows = kTokens * (rank + 1) / ranks - r0;
+  float* sums = ranks > 1 ? part + 128 * C::PITCH : part;
+  const int r0 = TOK * rank / ranks, rows = TOK * (rank + 1) / ranks - r0;
   if (ranks > 1) cluster.sync();
   else __syncthreads();
   for (int i = tid; i < rows * (BN / 4); i += kThreads) {
     const int row = i / (BN / 4), c = i % (BN / 4) * 4;
     if (m0 + r0 + row >= a.M) break;
+    const size_t at = (size_t)(r0 + row) * C::PITCH + c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ranks == 1) {
-      const float* p = part + (size_t)row * C::PITCH + c;
-      const float4 x = *reinterpret_cast<const float4*>(p);
-      const float4 y = *reinterpret_cast<const float4*>(p + (size_t)kTokens * C::PITCH);
-      v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-    } else {
-      const size_t hi = (size_t)(r0 + row) * C::PITCH + c, lo = hi + (size_t)kTokens * C::PITCH;
-      float4 x[8], y[8];
+    float4 x[8], y[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < ranks) {
-          const float* p = cluster.map_shared_rank(part, q);
-          x[q] = *reinterpret_cast<const float4*>(p + hi);
-          y[q] = *reinterpret_cast<const float4*>(p + lo);
-        }
+    for (int q = 0; q < 8; ++q)
+      if (q < ranks) {
+        const float* p = (ranks > 1 ? cluster.map_shared_rank(part, q) : part) + at;
+        x[q] = *reinterpret_cast<const float4*>(p);
+        y[q] = TOK == 64 ? *reinterpret_cast<const float4*>(p + 64 * C::PITCH) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < ranks)
-          v = make_float4(v.x + (x[q].x + y[q].x), v.y + (x[q].y + y[q].y), v.z + (x[q].z + y[q].z),
-                          v.w + (x[q].w + y[q].w));
-    }
+    for (int q = 0; q < 8; ++q)
+      if (q < ranks)
+        v = make_float4(v.x + (x[q].x + y[q].x), v.y + (x[q].y + y[q].y), v.z + (x[q].z + y[q].z),
+                        v.w + (x[q].w + y[q].w));
     *reinterpret_cast<float4*>(sums + (size_t)row * C::PITCH + c) = v;
   }
   if (ranks > 1) cluster.sync();  // the ranks' sums have been read: a rank may leave
@@ -442,13 +452,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// Tokens [M][E] fp16: boxes of 64 columns x 64 rows, 128-byte swizzle.
-bool token_map(CUtensorMap* tm, const void* base, int M, int E) {
+// Tokens [M][E] fp16: boxes of 64 columns x a tile's rows, 128-byte swizzle.
+bool token_map(CUtensorMap* tm, const void* base, int M, int E, int rows) {
   auto enc = encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)E, (cuuint64_t)M};
   const cuuint64_t strides[1] = {(cuuint64_t)E * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)kTokens}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)rows}, es[2] = {1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -500,23 +510,31 @@ int resident_clusters(const void* kern, int threads, size_t smem, int c) {
   return known[key] = n;
 }
 
-template <int R, int BN>
+// CTAs that split E for one tile: the most whose clusters all run at once, at
+// least two k-tiles each.
+template <int R, int BN, int TOK>
+int tile_ranks(int tiles, int KT) {
+  using C = BlockCfg<R, BN, TOK>;
+  const void* fn = reinterpret_cast<const void*>(block_gemm_kernel<R, BN, TOK>);
+  for (int c = 8; c > 1; --c)
+    if (2 * c <= KT && tiles * (long long)c <= kSMs && tiles <= resident_clusters(fn, C::kThreads, C::SMEM, c)) return c;
+  return 1;
+}
+
+template <int R, int BN, int TOK>
 cudaError_t launch_tiles(BlockArgs a, const __half* xhi, const __half* xlo, int E, const void* A_k, const void* A_v,
                          const PagedRows& place, cudaStream_t s) {
-  using C = BlockCfg<R, BN>;
-  auto kern = block_gemm_kernel<R, BN>;
+  using C = BlockCfg<R, BN, TOK>;
+  auto kern = block_gemm_kernel<R, BN, TOK>;
   const void* fn = reinterpret_cast<const void*>(kern);
   CUtensorMap mh, ml, mk, mv;
-  if (!token_map(&mh, xhi, a.M, E) || !token_map(&ml, xlo, a.M, E) || !weight_map(&mk, A_k, a.H, E, R, C::NG) ||
+  if (!token_map(&mh, xhi, a.M, E, TOK) || !token_map(&ml, xlo, a.M, E, TOK) || !weight_map(&mk, A_k, a.H, E, R, C::NG) ||
       !weight_map(&mv, A_v, a.H, E, R, C::NG))
     return cudaErrorInvalidValue;
   if (resident_clusters(fn, C::kThreads, C::SMEM, 1) < 1) return cudaErrorInvalidConfiguration;
-  const int mt = (a.M + kTokens - 1) / kTokens, nt = 2 * ((a.H * R + BN - 1) / BN);
+  const int mt = (a.M + TOK - 1) / TOK, nt = 2 * ((a.H * R + BN - 1) / BN);
   a.KT = E / kBK;
-  // The most ranks whose clusters all run at once, at least two k-tiles each.
-  a.ranks = 1;
-  for (int c = 8; c > 1 && a.ranks == 1; c >>= 1)
-    if (2 * c <= a.KT && (long long)mt * nt <= resident_clusters(fn, C::kThreads, C::SMEM, c)) a.ranks = c;
+  a.ranks = tile_ranks<R, BN, TOK>(mt * nt, a.KT);
   a.ctas = mt * a.ranks * nt;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -535,24 +553,40 @@ cudaError_t launch_tiles(BlockArgs a, const __half* xhi, const __half* xlo, int 
   return cudaLaunchKernelEx(&cfg, kern, mh, ml, mk, mv, a, place);
 }
 
-// Which tile.  The operand tiles come from L2 and bound the kernel once the CTAs
-// fill the device: 64 x 128 fetches 32 KB a k-tile, 64 x 256 48 KB for twice the
-// columns.  With half a wave of tiles or fewer the narrow ones keep more SMs at
-// work.  Measured, 128 / 256 columns in us (32 heads, E 4096): r 32, 16 tokens 15.4 /
-// 16.6, 128 18.2 / 22.3, 320 33.8 / 29.5, 576 36.6 / 32.8, 1728 102 / 95; r 64, 128
-// 23.1 / 23.9, 256 34.7 / 28.9, 576 68.1 / 44.9, 1728 195 / 127; r 128, 128 34.5 / 29.8;
-// r 16, 576 30.0 / 29.8, 1728 79.5 / 69.  (Tiles of 128 tokens x 128 columns took 50.5
-// for 576 tokens of r 32, 178 for 1728 of r 64; they led only for r 16 with E 2048,
-// 75.7 against 88.8 for 4096 tokens.)  Columns past a side's last head are idle: at most a quarter of them.
+// Which tile: 64 tokens x 128 columns, 64 x 256 or 128 x 256.  The operand tiles come
+// from L2 and bound the kernel once the CTAs fill the device: 32, 48 and 64 KB a
+// k-tile for 1, 2 and 4 times the products.
+//   Columns.  With half a wave of tiles or fewer the narrow ones keep more SMs at work.
+// Measured, 128 / 256 columns in us (32 heads, E 4096): r 32, 16 tokens 15.4 / 16.6, 128
+// 18.2 / 22.3, 320 33.8 / 29.5, 576 36.6 / 32.8, 1728 102 / 95; r 64, 128 23.1 / 23.9,
+// 256 34.7 / 28.9, 576 68.1 / 44.9, 1728 195 / 127; r 128, 128 34.5 / 29.8; r 16, 576
+// 30.0 / 29.8, 1728 79.5 / 69.  Columns past a side's last head are idle: at most a
+// quarter of them.
+//   Tokens.  Of the wide tiles, those whose waves end sooner: a k-tile takes 0.53 us of
+// 64 tokens, 0.86 of 128 (weighed 5 : 8).  Measured, 64 / 128 tokens: r 32, 400 tokens
+// 29.1 / 27.9, 576 30.7 / 35.0, 800 46.8 / 43.5, 1152 50.6 / 46.5, 1728 91 / 75, 4096
+// 195 / 160; r 64, 576 44.3 / 69, 1152 84 / 74, 1728 125 / 139, 4096 308 / 290; r 128,
+// 320 85 / 69, 576 84 / 124, 1152 163 / 141, 4096 627 / 510.
+//   Dropped: pairs of CTAs of 128 tokens that share their weight tile (cta_group::2):
+// a fresh accumulator per k-tile has to be read by both before the next but one, 1.37
+// us a k-tile; accumulators of four k-tiles, 0.9.  Sums of two k-tiles an accumulator
+// changed the single CTAs by less than 2 %.
 template <int R>
 cudaError_t launch_block(const BlockArgs& a, const __half* xhi, const __half* xlo, int E, const void* A_k,
                          const void* A_v, const PagedRows& place, cudaStream_t s) {
-  const int hr = a.H * R, sms = 148, mt = (a.M + kTokens - 1) / kTokens;
-  if ((long long)mt * 2 * ((hr + 127) / 128) > sms / 2 && 4 * ((hr + 255) / 256 * 256) <= 5 * hr)
-    return launch_tiles<R, 256>(a, xhi, xlo, E, A_k, A_v, place, s);
+  const int hr = a.H * R, KT = E / kBK, mt = (a.M + 63) / 64, n256 = 2 * ((hr + 255) / 256);
+  if ((long long)mt * 2 * ((hr + 127) / 128) > kSMs / 2 && 2 * n256 * 256 <= 5 * hr) {
+    const int few = mt * n256, tall = (mt + 1) / 2 * n256;  // tiles of 64, of 128 tokens
+    const auto span = [&](int tiles, int ranks) {
+      return (long long)((tiles * ranks + kSMs - 1) / kSMs) * ((KT + ranks - 1) / ranks);
+    };
+    if (8 * span(tall, tile_ranks<R, 256, 128>(tall, KT)) < 5 * span(few, tile_ranks<R, 256, 64>(few, KT)))
+      return launch_tiles<R, 256, 128>(a, xhi, xlo, E, A_k, A_v, place, s);
+    return launch_tiles<R, 256, 64>(a, xhi, xlo, E, A_k, A_v, place, s);
+  }
   if constexpr (R <= 64)
-    if (hr <= 64) return launch_tiles<R, 64>(a, xhi, xlo, E, A_k, A_v, place, s);
-  return launch_tiles<R, 128>(a, xhi, xlo, E, A_k, A_v, place, s);
+    if (hr <= 64) return launch_tiles<R, 64, 64>(a, xhi, xlo, E, A_k, A_v, place, s);
+  return launch_tiles<R, 128, 64>(a, xhi, xlo, E, A_k, A_v, place, s);
 }
 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
