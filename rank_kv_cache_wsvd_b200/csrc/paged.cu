@@ -10,6 +10,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <type_traits>
 
 #include "common.cuh"
 #include "paged.cuh"
@@ -52,6 +53,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
   const __half2 p = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// The next 16-bit part of two weights, which keep what is left: bf16 the upper
+// halves, so that three parts carry all 24 bits; fp16 rounded, two parts 22 bits.
+template <bool BF16>
+__device__ __forceinline__ uint32_t take_part(float& p0, float& p1) {
+  if constexpr (BF16) {
+    const uint32_t a = __float_as_uint(p0), b = __float_as_uint(p1);
+    p0 -= __uint_as_float(a & 0xffff0000u);
+    p1 -= __uint_as_float(b & 0xffff0000u);
+    return __byte_perm(a, b, 0x7632);
+  } else {
+    const uint32_t x = pack2<BF16>(p0, p1);
+    const float2 f = unpack2<BF16>(x);
+    p0 -= f.x;
+    p1 -= f.y;
+    return x;
+  }
 }
 
 // The rotation of 8 pairs (a_i, b_i): a' = a cos - b sin, b' = b cos + a sin,
@@ -208,11 +227,11 @@ __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArg
 // (16-byte chunks, swizzled so that ldmatrix reads no bank twice) and needs no
 // barrier until the segment ends.
 //
-// Per strip, with m16n8k16 products (rows x queries, so up to 8 queries cost
-// one column block, and GQA reads the rows once for all of them):
-//   S = K q^T         K as the row operand, q^T held in registers
+// Per strip, with m16n8k16 products (up to 8 queries as their columns, up to 16 as
+// their rows, so GQA reads the rows once for all of them):
+//   S = K q^T (or q K^T)       the queries held in registers
 //   p = 2^(S * scale * log2 e - m), m the running maximum of the warp's rows
-//   O^T += V^T p^T    V^T by transposed ldmatrix, p^T by movmatrix
+//   O^T += V^T p^T (or P V)    V by transposed ldmatrix
 // p is not rounded to the 16-bit type: it is cut into parts whose sum carries
 // 22 (two fp16 parts) or 24 bits (three bf16 parts), each its own product.
 // The products cost less than the rows' bytes for up to 16 queries.
@@ -220,11 +239,11 @@ template <bool BF16, int HD, int NB>
 struct DecCfg {
   // Rows per strip, warps per CTA and stages per warp: strips of 8 KB (16 KB at
   // head size 256), 192 KB of them per SM.  Twelve warps of two stages beat
-  // eight of three (4 x 32768 rows of 8 heads of 128: 84.7 us against 87.3; 64
-  // with 16 queries a head, 9 x 32768 rows: 56.6 against 63.4) except where two
-  // column blocks of head size 128 leave registers for eight warps only (twelve,
-  // spilling: 109.3 against 107.3).  Strips of half the size need more warps for
-  // the same bytes and lose (64, sixteen warps of three: 66.0).
+  // eight of three (4 x 32768 rows of 8 heads of 128: 84.7 us against 87.3) except with
+  // 16 queries of head size 128 and their registers (16 sequences of 1024 .. 4096 rows
+  // of 8 heads 41.5 against 38.8, 4 x 32768 rows 92.7 against 94.5).  Strips of half the
+  // size need more warps for the same bytes and lose (16 queries of head size 64 as
+  // columns, 9 x 32768 rows: sixteen warps of three 66.0 against 56.6).
   static constexpr bool kWide = HD == 128 && NB == 2;
   static constexpr int kTS = HD >= 128 ? 16 : (HD == 64 ? 32 : 64);
   static constexpr int kWarps = HD == 256 ? 6 : kWide ? 8 : 12;
@@ -285,6 +304,399 @@ __device__ __forceinline__ uint32_t strip_off(int r, int c) {
   return (uint32_t)(r * HD * 2 + ((c ^ (r & 7)) << 4));
 }
 
+// The same product into D = 0 + A B.
+template <bool BF16>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// (x0, x1) = (x0, x1) f + (y0, y1), one instruction.
+__device__ __forceinline__ void fma2(float& x0, float& x1, float f, float y0, float y1) {
+  asm("{\n\t.reg .b64 x, f, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "fma.rn.f32x2 x, x, f, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(f), "f"(y0), "f"(y1));
+}
+
+// Whether a strip of `bytes` at vb holds an infinity or a NaN (the whole warp asks).
+template <bool BF16>
+__device__ __forceinline__ bool any_wild(uint32_t vb, int bytes, int lane) {
+  bool wild = false;
+  for (int i = lane; i < bytes / 16; i += 32) {
+    const uint4 w = lds128(vb + (uint32_t)i * 16);
+    const uint32_t e = BF16 ? 0x7f80u : 0x7c00u, e2 = e << 16;
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) wild |= (ws[k] & e) == e || (ws[k] & e2) == e2;
+  }
+  return __any_sync(0xffffffffu, wild);
+}
+
+// Up to eight queries of a warp, as the columns of the products: S = K q^T, O^T += V^T p^T.
+template <bool BF16, int HD>
+struct Queries8 {
+  using C = DecCfg<BF16, HD, 1>;
+  static constexpr int TS = C::kTS, MT = C::kMT, KS = HD / 16, NP = C::kParts;
+  static constexpr float kBias = BF16 ? 0.f : 12.f;
+  uint32_t q[KS][2];
+  int lim[2], lim_min;              // rows that query 2 c4 + i sees
+  float scale, m[2], l[2], o[KS][4];  // o: dims 16 d + g, then + 8, of queries 2 c4 + {0, 1}
+
+  __device__ __forceinline__ void begin(const KvDecodeArgs& a, int b, int n, int h, int j0, int nq, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+    lim_min = n - a.Tq + 1;
+    scale = a.qscale;
+    const int jq = j0 + (g < nq ? g : 0);
+    const uint16_t* qr = a.q + (((size_t)b * a.Tq + jq / a.G) * a.Hq + h * a.G + jq % a.G) * HD + 2 * c4;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      q[k][0] = g < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k)) : 0u;
+      q[k][1] = g < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8)) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lim[i] = lim_min + min(j0 + 2 * c4 + i, a.nq - 1) / a.G;
+      m[i] = kNegInf;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < KS; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+  }
+
+  __device__ __forceinline__ void strip(const KvDecodeArgs& a, uint32_t kb, uint32_t vb, int l0, int valid, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+    // Two sums (even and odd steps of 16 values), so that consecutive products
+    // do not wait for one another.
+    float sc[MT][4], sc2[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[t][i] = sc2[t][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        uint32_t kf[4];
+        ldsm4(kf, kb + strip_off<HD>(t * 16 + (lane & 15), 2 * k + (lane >> 4)));
+        mma16816<BF16>(k & 1 ? sc2[t] : sc[t], kf, q[k][0], q[k][1]);
+      }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[t][i] = (sc[t][i] + sc2[t][i]) * scale;
+    const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = l0 + t * 16 + g + (i >> 1) * 8;
+          if (row >= lim[i & 1] || !((valid >> t) & 1)) sc[t][i] = kNegInf;
+        }
+    }
+    // Running maximum and sum; columns (queries) of sc and o are the same.
+    float alpha[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = kNegInf;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) mx = fmaxf(mx, fmaxf(sc[t][i], sc[t][i + 2]));
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mn = fmaxf(m[i], mx);
+      const float ref = mn == kNegInf ? 0.f : mn;
+      alpha[i] = ex2(m[i] - ref);
+      m[i] = mn;
+      float add = 0.f;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          const float p = ex2(sc[t][i + r] - ref + kBias);
+          sc[t][i + r] = p;
+          add += p;
+        }
+      l[i] = l[i] * alpha[i] + add;
+    }
+    if (masked && a.Tq > 1 && any_wild<BF16>(vb, C::kHalf, lane)) {  // as for 16 queries, row by row
+#pragma unroll
+      for (int d = 0; d < KS; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] *= alpha[i & 1];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll 1
+        for (int r = 0; r < 16; ++r) {
+          const int row = l0 + t * 16 + r, from = (r & 7) * 4 + c4;
+          const float p00 = __shfl_sync(0xffffffffu, sc[t][0], from);
+          const float p01 = __shfl_sync(0xffffffffu, sc[t][1], from);
+          const float p10 = __shfl_sync(0xffffffffu, sc[t][2], from);
+          const float p11 = __shfl_sync(0xffffffffu, sc[t][3], from);
+          const float p[2] = {r < 8 ? p00 : p10, r < 8 ? p01 : p11};
+#pragma unroll
+          for (int d = 0; d < KS; ++d)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint16_t w;
+              asm volatile("ld.shared.u16 %0, [%1];"
+                           : "=h"(w)
+                           : "r"(vb + strip_off<HD>(t * 16 + r, 2 * d + half) + 2u * g)
+                           : "memory");
+              const float v = BF16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (row < lim[i]) o[d][2 * half + i] = fmaf(p[i], v, o[d][2 * half + i]);
+            }
+        }
+      return;
+    }
+    uint32_t pf[MT][NP][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      float r0 = sc[t][0], r1 = sc[t][1], r2 = sc[t][2], r3 = sc[t][3];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        pf[t][k][0] = movm_t(take_part<BF16>(r0, r1));
+        pf[t][k][1] = movm_t(take_part<BF16>(r2, r3));
+      }
+    }
+    constexpr int DG = 4 < KS ? 4 : KS;  // sums that start at zero, as for 16 queries
+#pragma unroll
+    for (int d0 = 0; d0 < KS; d0 += DG) {
+      float part[DG][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        uint32_t vf[DG][4];
+#pragma unroll
+        for (int d = 0; d < DG; ++d)
+          ldsm4_t(vf[d], vb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * (d0 + d) + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+          for (int d = 0; d < DG; ++d) {
+            if (t == 0 && k == 0) mma16816_first<BF16>(part[d], vf[d], pf[t][k][0], pf[t][k][1]);
+            else mma16816<BF16>(part[d], vf[d], pf[t][k][0], pf[t][k][1]);
+          }
+      }
+#pragma unroll
+      for (int d = 0; d < DG; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d0 + d][i] = fmaf(o[d0 + d][i], alpha[i & 1], part[d][i]);
+    }
+  }
+
+  __device__ __forceinline__ void leave(float* scratch, float* sm_m, float* sm_l, int lane) const {
+    const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v = l[i];
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+      const int j = 2 * c4 + i;
+      if (g == 0) {
+        sm_m[j] = m[i];
+        sm_l[j] = v;
+      }
+#pragma unroll
+      for (int d = 0; d < KS; ++d) {
+        scratch[j * HD + ((d * 16 + g) ^ (c4 << 3))] = o[d][i];
+        scratch[j * HD + ((d * 16 + 8 + g) ^ (c4 << 3))] = o[d][2 + i];
+      }
+    }
+  }
+};
+
+// Up to 16 queries of a warp, as the rows of the products: S = q K^T, O += P V.
+// The scores' registers are the second product's operand as they lie (no
+// movmatrix), and a query's maximum crosses four lanes: 561 instructions a strip (32
+// rows, head size 64), 762 as two column blocks of the form for eight.  28 queries
+// of 4 heads of 64, 9 x 32768 rows: 81 us against 101; 16 of 8 heads of 128, 4 x 32768
+// rows: 93 against 95.6.
+template <bool BF16, int HD>
+struct Queries16 {
+  using C = DecCfg<BF16, HD, 2>;
+  static constexpr int TS = C::kTS, MT = C::kMT, KS = HD / 16, NP = C::kParts;
+  // 2^bias keeps the low fp16 part of small weights out of the denormals.
+  static constexpr float kBias = BF16 ? 0.f : 12.f;
+  uint32_t q[KS][4];
+  int lim[2], lim_min;             // rows that query g + 8 i sees
+  float scale, m[2], l[2], o[HD / 8][4];  // o: dims 8 n + 2 c4 + {0, 1} of query g, then of g + 8
+
+  __device__ __forceinline__ void begin(const KvDecodeArgs& a, int b, int n, int h, int j0, int nq, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+    lim_min = n - a.Tq + 1;
+    scale = fabsf(a.qscale);  // its sign goes into the queries
+    const uint32_t flip = a.qscale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = g + 8 * i, jq = j0 + (j < nq ? j : 0);
+      const uint16_t* qr = a.q + (((size_t)b * a.Tq + jq / a.G) * a.Hq + h * a.G + jq % a.G) * HD + 2 * c4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        q[k][i] = j < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k)) ^ flip : 0u;
+        q[k][2 + i] = j < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8)) ^ flip : 0u;
+      }
+      lim[i] = lim_min + min(j0 + j, a.nq - 1) / a.G;
+      m[i] = kNegInf;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+  }
+
+  // The strip of rows l0 .. at kb and vb; bit t of valid: 16 rows whose page is in the pool.
+  __device__ __forceinline__ void strip(const KvDecodeArgs& a, uint32_t kb, uint32_t vb, int l0, int valid, int lane) {
+    const int c4 = lane & 3;
+    float sc[2 * MT][4];
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        uint32_t f[4];
+        ldsm4(f, kb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (k == 0) mma16816_first<BF16>(sc[2 * t + x], q[k], f[2 * x], f[2 * x + 1]);
+          else mma16816<BF16>(sc[2 * t + x], q[k], f[2 * x], f[2 * x + 1]);
+        }
+      }
+    const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < 2 * MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (l0 + t * 8 + 2 * c4 + (i & 1) >= lim[i >> 1] || !((valid >> (t / 2)) & 1)) sc[t][i] = kNegInf;
+    }
+    float alpha[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = kNegInf;
+#pragma unroll
+      for (int t = 0; t < 2 * MT; ++t) mx = fmaxf(mx, fmaxf(sc[t][2 * i], sc[t][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[i], mx * scale);
+      const float ref = mn == kNegInf ? 0.f : mn;
+      alpha[i] = ex2(m[i] - ref);
+      m[i] = mn;
+      float add0 = 0.f, add1 = 0.f;
+      const float sub = kBias - ref;
+#pragma unroll
+      for (int t = 0; t < 2 * MT; ++t) {
+        fma2(sc[t][2 * i], sc[t][2 * i + 1], scale, sub, sub);
+        sc[t][2 * i] = ex2(sc[t][2 * i]);
+        sc[t][2 * i + 1] = ex2(sc[t][2 * i + 1]);
+        add0 += sc[t][2 * i];
+        add1 += sc[t][2 * i + 1];
+      }
+      l[i] = fmaf(l[i], alpha[i], add0 + add1);
+    }
+    // A later token's value may be infinite or NaN; it must not reach the
+    // queries that do not see it (0 * NaN), so such a strip is summed row by
+    // row.  Rows past the length are zero already.
+    if (masked && a.Tq > 1 && any_wild<BF16>(vb, C::kHalf, lane)) {
+#pragma unroll
+      for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] *= alpha[i >> 1];
+#pragma unroll
+      for (int t = 0; t < 2 * MT; ++t)
+#pragma unroll 1
+        for (int r = 0; r < 8; ++r) {
+          float p[4];  // query g and g + 8 of row r: even and odd rows lie in different registers
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xffffffffu, sc[t][i], (lane & ~3) | (r >> 1));
+          const float w[2] = {r & 1 ? p[1] : p[0], r & 1 ? p[3] : p[2]};
+          const int row = t * 8 + r;
+#pragma unroll
+          for (int d = 0; d < HD / 8; ++d) {
+            const float2 v = unpack2<BF16>(lds32(vb + strip_off<HD>(row, d) + 4u * c4));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (l0 + row < lim[i]) {
+                o[d][2 * i] = fmaf(w[i], v.x, o[d][2 * i]);
+                o[d][2 * i + 1] = fmaf(w[i], v.y, o[d][2 * i + 1]);
+              }
+          }
+        }
+      return;
+    }
+    uint32_t pf[MT][NP][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // query g (x even) or g + 8, rows 2 c4 + {0, 1} (x < 2) or eight on
+        float p0 = sc[2 * t + x / 2][2 * (x & 1)], p1 = sc[2 * t + x / 2][2 * (x & 1) + 1];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) pf[t][k][x] = take_part<BF16>(p0, p1);
+      }
+    // Each strip's product starts at zero and joins O in fp32: the tensor
+    // cores' own sums do not round to nearest, and over a long cache that
+    // bias would show (3e-6 of the output at 32768 rows, 4e-7 this way).
+    // Several dim blocks at a time, for products that do not wait for one another.
+    constexpr int DG = 2;
+#pragma unroll
+    for (int d0 = 0; d0 < KS; d0 += DG) {
+      float part[2 * DG][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        uint32_t f[DG][4];
+#pragma unroll
+        for (int d = 0; d < DG; ++d) ldsm4_t(f[d], vb + strip_off<HD>(t * 16 + (lane & 15), 2 * (d0 + d) + (lane >> 4)));
+#pragma unroll
+        for (int k = 0; k < NP; ++k)
+#pragma unroll
+          for (int d = 0; d < 2 * DG; ++d) {
+            if (t == 0 && k == 0) mma16816_first<BF16>(part[d], pf[t][k], f[d / 2][2 * (d & 1)], f[d / 2][2 * (d & 1) + 1]);
+            else mma16816<BF16>(part[d], pf[t][k], f[d / 2][2 * (d & 1)], f[d / 2][2 * (d & 1) + 1]);
+          }
+      }
+#pragma unroll
+      for (int d = 0; d < 2 * DG; ++d)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          fma2(o[2 * d0 + d][2 * i], o[2 * d0 + d][2 * i + 1], alpha[i], part[d][2 * i], part[d][2 * i + 1]);
+    }
+  }
+
+  // O as [query][dim] with bits 3 and 4 of dim turned by the query, and the statistics.
+  __device__ __forceinline__ void leave(float* scratch, float* sm_m, float* sm_l, int lane) const {
+    const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v = l[i];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      const int j = g + 8 * i;
+      if (c4 == 0) {
+        sm_m[j] = m[i];
+        sm_l[j] = v;
+      }
+#pragma unroll
+      for (int d = 0; d < HD / 8; ++d)
+        *reinterpret_cast<float2*>(scratch + j * HD + ((d * 8 + 2 * c4) ^ (((j >> 1) & 3) << 3))) =
+            make_float2(o[d][2 * i], o[d][2 * i + 1]);
+    }
+  }
+};
+
 // Strips that a segment's fixed cost counts as.  Measured (a ragged batch with
 // four tokens a sequence, 0 / 8 / 16 / 24 strips): 33.9 / 26.3 / 25.6 / 25.9 us; 32
 // heads of 1600 rows 12.4 / 11.7 / 10.6 / 10.6 us.
@@ -306,9 +718,7 @@ constexpr int kMaxSolo = 2048;  // workers that way at most; sizes the partials
 template <bool BF16, int HD, int NB, bool MANY>
 __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_kernel(const KvDecodeArgs a) {
   using C = DecCfg<BF16, HD, NB>;
-  constexpr int TS = C::kTS, MT = C::kMT, S = C::kStages, NW = C::kWarps, KS = HD / 16, NP = C::kParts;
-  // 2^bias keeps the low fp16 part of small weights out of the denormals.
-  constexpr float kBias = BF16 ? 0.f : 12.f;
+  constexpr int TS = C::kTS, MT = C::kMT, S = C::kStages, NW = C::kWarps;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sm_m[NW][C::kQ], sm_l[NW][C::kQ];
   __shared__ int sm_valid[NW][S];
@@ -339,6 +749,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
   auto ld = seg;
   int ls = ld.s + first;
+  int lh = ld.u / a.chunks;  // its KV head
   bool more = true;
   int pg[MT];
   const int page_mask = (1 << a.page_shift) - 1;
@@ -346,6 +757,7 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     while (more && ls >= ld.e) {
       more = ld.next(seqs);
       ls = ld.s + first;
+      lh = ld.u / a.chunks;
     }
     if (more) {
 #pragma unroll
@@ -358,7 +770,6 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   auto issue = [&](int stage) {
     if (more) {
       const uint32_t dst = my_ring + (uint32_t)stage * C::kStage;
-      const int h = ld.u / a.chunks;
       int valid = 0;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -366,17 +777,16 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
         const bool in = pg[i] >= 0 && pg[i] < a.num_pages;
         if (!in && lane == 0 && l0 < ld.n) set_err(a.err, WSVD_DEVERR_PAGE_RANGE);
         valid |= (in ? 1 : 0) << i;
-        const size_t row0 = (((size_t)(in ? pg[i] : 0) * a.Hkv + h) << a.page_shift) + (l0 & page_mask);
+        const size_t row0 = (((size_t)(in ? pg[i] : 0) * a.Hkv + lh) << a.page_shift) + (l0 & page_mask);
         const int rows = in ? ld.n - l0 : 0;  // rows at and past the length are zero-filled, not read
         constexpr int kPer = 16 * C::kChunks / 32;
+        const uint16_t *ks = a.k + row0 * HD + lane * 8, *vs = a.v + row0 * HD + lane * 8;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const int idx = j * 32 + lane, r = idx / C::kChunks, ch = idx % C::kChunks;
-          const uint32_t off = strip_off<HD>(i * 16 + r, ch);
-          const bool there = r < rows;
-          const size_t src = (row0 + (there ? r : 0)) * HD + ch * 8;
-          cp_async16(dst + off, a.k + src, there ? 16u : 0u);
-          cp_async16(dst + C::kHalf + off, a.v + src, there ? 16u : 0u);
+          const uint32_t to = dst + strip_off<HD>(i * 16 + r, ch), bytes = r < rows ? 16u : 0u;
+          cp_async16(to, ks + j * 256, bytes);
+          cp_async16(to + C::kHalf, vs + j * 256, bytes);
         }
       }
       if (lane == 0) sm_valid[warp][stage] = valid;
@@ -394,201 +804,17 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     if (seg.s == seg.e) continue;
     const int h = seg.u / a.chunks, j0 = (seg.u % a.chunks) * C::kQ;
     const int nq = min(C::kQ, a.nq - j0);
-    uint32_t qf[NB][KS][2];
-    int lim[NB][2];  // rows that query 2 * c4 + {0, 1} of a block sees
     const int lim_min = seg.n - a.Tq + 1;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int j = nb * 8 + g;
-      const int jq = j0 + (j < nq ? j : 0);
-      const uint16_t* qr = a.q + (((size_t)seg.b * a.Tq + jq / a.G) * a.Hq + h * a.G + jq % a.G) * HD + 2 * c4;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qf[nb][k][0] = j < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k)) : 0u;
-        qf[nb][k][1] = j < nq ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8)) : 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) lim[nb][i] = lim_min + min(j0 + nb * 8 + 2 * c4 + i, a.nq - 1) / a.G;
-    }
-    float m[NB][2], l[NB][2], o[KS][NB][4];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      m[nb][0] = m[nb][1] = kNegInf;
-      l[nb][0] = l[nb][1] = 0.f;
-#pragma unroll
-      for (int d = 0; d < KS; ++d) o[d][nb][0] = o[d][nb][1] = o[d][nb][2] = o[d][nb][3] = 0.f;
-    }
+    typename std::conditional<NB == 1, Queries8<BF16, HD>, Queries16<BF16, HD>>::type acc;
+    acc.begin(a, seg.b, seg.n, h, j0, nq, lane);
 
     int last_stage = stage == 0 ? S - 1 : stage - 1;  // a stage with nothing in it or on its way
     for (int s = seg.s + first; s < seg.e; s += stride) {
       cp_wait<S - 2>();
       __syncwarp();
       issue(stage == 0 ? S - 1 : stage - 1);
-      const uint32_t kb = my_ring + (uint32_t)stage * C::kStage, vb = kb + C::kHalf;
-      // Two sums per column block (even and odd steps of 16 values), so that
-      // consecutive products do not wait for one another.
-      float sc[MT][NB][4], sc2[MT][NB][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[t][nb][i] = sc2[t][nb][i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          uint32_t kf[4];
-          ldsm4(kf, kb + strip_off<HD>(t * 16 + (lane & 15), 2 * k + (lane >> 4)));
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma16816<BF16>(k & 1 ? sc2[t][nb] : sc[t][nb], kf, qf[nb][k][0], qf[nb][k][1]);
-        }
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[t][nb][i] = (sc[t][nb][i] + sc2[t][nb][i]) * a.qscale;
-      const int l0 = s * TS, valid = sm_valid[warp][stage];
-      const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
-      if (masked) {
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = l0 + t * 16 + g + (i >> 1) * 8;
-              if (row >= lim[nb][i & 1] || !((valid >> t) & 1)) sc[t][nb][i] = kNegInf;
-            }
-      }
-      // Running maximum and sum; columns (queries) of sc and o are the same.
-      uint32_t pf[MT][NB][NP][2];
-      float alpha[NB][2];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = kNegInf;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) mx = fmaxf(mx, fmaxf(sc[t][nb][i], sc[t][nb][i + 2]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-          const float mn = fmaxf(m[nb][i], mx);
-          const float ref = mn == kNegInf ? 0.f : mn;
-          alpha[nb][i] = ex2(m[nb][i] - ref);
-          m[nb][i] = mn;
-          float add = 0.f;
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-              const float p = ex2(sc[t][nb][i + r] - ref + kBias);
-              sc[t][nb][i + r] = p;
-              add += p;
-            }
-          l[nb][i] = l[nb][i] * alpha[nb][i] + add;
-        }
-      // A later token's value may be infinite or NaN; it must not reach the
-      // queries that do not see it (0 * NaN), so such a strip is summed row by
-      // row.  Rows past the length are zero already.
-      bool wild = false;
-      if (masked && a.Tq > 1) {
-        for (int i = lane; i < TS * C::kChunks; i += 32) {
-          const uint4 w = lds128(vb + (uint32_t)i * 16);
-          const uint32_t e = BF16 ? 0x7f80u : 0x7c00u, e2 = e << 16;
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) wild |= (ws[k] & e) == e || (ws[k] & e2) == e2;
-        }
-        wild = __any_sync(0xffffffffu, wild);
-      }
-      if (wild) {
-#pragma unroll
-        for (int d = 0; d < KS; ++d)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[d][nb][i] *= alpha[nb][i & 1];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll 1
-          for (int r = 0; r < 16; ++r) {
-            const int row = l0 + t * 16 + r;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              const int from = (r & 7) * 4 + c4;
-              const float p00 = __shfl_sync(0xffffffffu, sc[t][nb][0], from);
-              const float p01 = __shfl_sync(0xffffffffu, sc[t][nb][1], from);
-              const float p10 = __shfl_sync(0xffffffffu, sc[t][nb][2], from);
-              const float p11 = __shfl_sync(0xffffffffu, sc[t][nb][3], from);
-              const float p[2] = {r < 8 ? p00 : p10, r < 8 ? p01 : p11};
-#pragma unroll
-              for (int d = 0; d < KS; ++d)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  uint16_t w;
-                  asm volatile("ld.shared.u16 %0, [%1];"
-                               : "=h"(w)
-                               : "r"(vb + strip_off<HD>(t * 16 + r, 2 * d + half) + 2u * g)
-                               : "memory");
-                  const float v = BF16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
-#pragma unroll
-                  for (int i = 0; i < 2; ++i)
-                    if (row < lim[nb][i]) o[d][nb][2 * half + i] = fmaf(p[i], v, o[d][nb][2 * half + i]);
-                }
-            }
-          }
-      } else {
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float r0 = sc[t][nb][0], r1 = sc[t][nb][1], r2 = sc[t][nb][2], r3 = sc[t][nb][3];
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-              const uint32_t x = pack2<BF16>(r0, r1), y = pack2<BF16>(r2, r3);
-              pf[t][nb][k][0] = movm_t(x);
-              pf[t][nb][k][1] = movm_t(y);
-              const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
-              r0 -= fx.x; r1 -= fx.y; r2 -= fy.x; r3 -= fy.y;
-            }
-          }
-        // Each strip's product starts at zero and joins O in fp32: the tensor
-        // cores' own sums do not round to nearest, and over a long cache that
-        // bias would show (3e-6 of the output at 32768 rows, 4e-7 this way).
-        // Several dim blocks at a time, for products that do not wait for one another.
-        constexpr int DG = KS < 4 ? KS : 4 / NB;
-#pragma unroll
-        for (int d0 = 0; d0 < KS; d0 += DG) {
-          float part[DG][NB][4];
-#pragma unroll
-          for (int d = 0; d < DG; ++d)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) part[d][nb][0] = part[d][nb][1] = part[d][nb][2] = part[d][nb][3] = 0.f;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            uint32_t vf[DG][4];
-#pragma unroll
-            for (int d = 0; d < DG; ++d)
-              ldsm4_t(vf[d], vb + strip_off<HD>(t * 16 + ((lane >> 4) << 3) + (lane & 7),
-                                                2 * (d0 + d) + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int k = 0; k < NP; ++k)
-#pragma unroll
-              for (int d = 0; d < DG; ++d)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma16816<BF16>(part[d][nb], vf[d], pf[t][nb][k][0], pf[t][nb][k][1]);
-          }
-#pragma unroll
-          for (int d = 0; d < DG; ++d)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[d0 + d][nb][i] = fmaf(o[d0 + d][nb][i], alpha[nb][i & 1], part[d][nb][i]);
-        }
-      }
+      const uint32_t kb = my_ring + (uint32_t)stage * C::kStage;
+      acc.strip(a, kb, kb + C::kHalf, s * TS, sm_valid[warp][stage], lane);
       __syncwarp();  // every lane has read this stage before it is filled again
       last_stage = stage;
       stage = stage == S - 1 ? 0 : stage + 1;
@@ -649,10 +875,10 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
       }
     };
 
-    if (MANY && solo) {  // ---- one warp's result: straight to out, or to its partial slot
+    if constexpr (MANY) if (solo) {  // ---- one warp's result: straight to out, or to its partial slot
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float L = l[0][i];
+        float L = acc.l[i];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
         const int j = 2 * c4 + i;
@@ -662,11 +888,11 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
         const bool sees = lim_min + t > 0;
         const float f = whole ? 1.f / L : 1.f;
 #pragma unroll
-        for (int d = 0; d < KS; ++d) {
-          __stcg(to + d * 16 + g, whole && !sees ? 0.f : o[d][0][i] * f);
-          __stcg(to + d * 16 + 8 + g, whole && !sees ? 0.f : o[d][0][2 + i] * f);
+        for (int d = 0; d < HD / 16; ++d) {
+          __stcg(to + d * 16 + g, whole && !sees ? 0.f : acc.o[d][i] * f);
+          __stcg(to + d * 16 + 8 + g, whole && !sees ? 0.f : acc.o[d][2 + i] * f);
         }
-        if (!whole && g == 0) __stcg(reinterpret_cast<float2*>(part + qmax * HD + 2 * j), make_float2(m[0][i], L));
+        if (!whole && g == 0) __stcg(reinterpret_cast<float2*>(part + qmax * HD + 2 * j), make_float2(acc.m[i], L));
       }
       if (whole) continue;
       int wf, np, last = 0;
@@ -682,27 +908,10 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     }
 
     // ---- the warps' results of this segment, joined.  Each warp leaves O in
-    // its free stage, [query][dim] with bits 3 and 4 of dim turned by the lane
+    // its free stage, [query][dim] with bits 3 and 4 of dim turned by the query
     // so that the stores meet no bank twice and float4 reads stay whole.
     float* scratch = reinterpret_cast<float*>(ring) + (size_t)(warp * S + last_stage) * (C::kStage / 4);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v = l[nb][i];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-        const int j = nb * 8 + 2 * c4 + i;
-        if (g == 0) {
-          sm_m[warp][j] = m[nb][i];
-          sm_l[warp][j] = v;
-        }
-#pragma unroll
-        for (int d = 0; d < KS; ++d) {
-          scratch[j * HD + ((d * 16 + g) ^ (c4 << 3))] = o[d][nb][i];
-          scratch[j * HD + ((d * 16 + 8 + g) ^ (c4 << 3))] = o[d][nb][2 + i];
-        }
-      }
+    acc.leave(scratch, sm_m[warp], sm_l[warp], lane);
     if (lane == 0) sm_slot[warp] = warp * S + last_stage;
     __syncthreads();
     for (int idx = tid; idx < nq * (HD / 4); idx += C::kThreads) {
@@ -757,10 +966,10 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Queries per chunk: two column blocks of 8, one at head size 256 (registers).
-// Four blocks at head sizes 32 and 64, which read the rows once for 32 queries,
-// gave nothing (28 queries, 9 x 32768 rows of 4 heads of 64: 97.0 us against
-// 98.8; 9 ragged sequences 26.4 against 24.3): the products bound these, not the
-// second read of the rows from L2.
+// Two sixteens over one copy of the rows at head sizes 32 and 64 (eight warps, three
+// stages) gain for long sequences what they lose for short ones: 28 queries of 4 heads
+// of 64, 9 x 32768 rows 78.5 us against 86.5 (81 since), 9 ragged sequences 21.3 / 21.0, of 64
+// rows 7.6 / 6.5.
 inline int chunk_queries(int nq, int Hd) { return nq > 8 && Hd != 256 ? 16 : 8; }
 
 using DecodeFn = void (*)(const KvDecodeArgs);
