@@ -749,15 +749,15 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
   const uint32_t my_ring = smem_u32(ring) + (uint32_t)warp * S * C::kStage;
   auto ld = seg;
   int ls = ld.s + first;
-  int lh = ld.u / a.chunks;  // its KV head
-  bool more = true;
+  int lh = 0;  // its KV head
+  bool more = true, moved = true;
   int pg[MT];
   const int page_mask = (1 << a.page_shift) - 1;
   auto settle = [&]() {  // the next strip of this warp, and its pages
     while (more && ls >= ld.e) {
       more = ld.next(seqs);
       ls = ld.s + first;
-      lh = ld.u / a.chunks;
+      moved = true;
     }
     if (more) {
 #pragma unroll
@@ -765,6 +765,8 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
         const int l = ls * TS + i * 16;
         pg[i] = l < ld.n ? __ldg(a.block_table + (size_t)ld.b * a.max_pages + (l >> a.page_shift)) : 0;
       }
+      if (moved) lh = ld.u / a.chunks;  // while the page ids arrive
+      moved = false;
     }
   };
   auto issue = [&](int stage) {
@@ -965,7 +967,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-// Queries per chunk: two column blocks of 8, one at head size 256 (registers).
+// Queries per chunk: 16, at head size 256 eight (registers).
 // Two sixteens over one copy of the rows at head sizes 32 and 64 (eight warps, three
 // stages) gain for long sequences what they lose for short ones: 28 queries of 4 heads
 // of 64, 9 x 32768 rows 78.5 us against 86.5 (81 since), 9 ragged sequences 21.3 / 21.0, of 64
