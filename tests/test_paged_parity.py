@@ -145,6 +145,58 @@ def test_decode_nan_stays_where_it_is_seen(dtype):
     assert torch.isnan(bad[hit]).all() and torch.equal(bad[~hit], good[~hit])
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("Hd", [32, 64, 128, 256])
+@pytest.mark.parametrize("G,Tq", [(9, 1), (4, 4), (5, 7)])
+@pytest.mark.parametrize("scale", [-0.2, 0.5])
+def test_decode_many_queries_a_head_with_either_sign_of_scale(dtype, Hd, G, Tq, scale):
+    """Nine queries and more, whose products turn the sign of the scale into the
+    queries; logits of some tens, so that the running maximum moves."""
+    lens = [200, 77, 2]
+    kp, vp, table = _cache(lens, 2, Hd, 16, dtype, seed=31)
+    q = randn((3, Tq, 2 * G, Hd), dtype, 32)
+    out, err = _decode(q, kp, vp, table, lens, softmax_scale=scale)
+    assert err == 0
+    _check_decode(out, q, kp.nan_to_num(0), vp.nan_to_num(0), table, lens, scale, f"Hd{Hd} G{G} Tq{Tq} scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("Hd", [32, 64, 128])
+@pytest.mark.parametrize("G,Tq", [(1, 3), (16, 2), (7, 4)])
+def test_decode_wild_later_rows_with_few_and_many_queries(dtype, Hd, G, Tq):
+    """The last row holds infinities and NaN: only the last token's queries see it."""
+    lens = [18, 64, 131]
+    kp, vp, table = _cache(lens, 2, Hd, 32, dtype, seed=41)
+    clean = (kp.clone(), vp.clone())
+    for i, n in enumerate(lens):
+        l = n - 1
+        kp[table[i, l // 32], :, l % 32] = (float("inf"), float("-inf"), NAN)[i]
+        vp[table[i, l // 32], :, l % 32] = (NAN, float("inf"), float("-inf"))[i]
+    q = randn((3, Tq, 2 * G, Hd), dtype, 42)
+    out, err = _decode(q, kp, vp, table, lens)
+    assert err == 0
+    got = out[:, : Tq - 1].double().cpu().numpy()
+    ref, mass, wobble = P.decode(f64(q), f64(clean[0].nan_to_num(0)), f64(clean[1].nan_to_num(0)), table, lens)
+    allow = P.decode_allowance(mass, wobble, Hd, max(lens))[:, : Tq - 1]
+    assert np.isfinite(got).all() and (np.abs(got - ref[:, : Tq - 1]) <= allow).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_decode_nan_stays_with_its_query_of_sixteen(dtype):
+    """A NaN query among sixteen of a head makes its own output NaN and no other."""
+    lens = [70, 33]
+    kp, vp, table = _cache(lens, 2, 64, 16, dtype, seed=5)
+    q = randn((2, 1, 32, 64), dtype, 6)
+    good, _ = _decode(q, kp, vp, table, lens)
+    q2 = q.clone()
+    q2[0, 0, 5, 9] = q2[1, 0, 29, 60] = NAN
+    bad, err = _decode(q2, kp, vp, table, lens)
+    assert err == 0
+    hit = torch.zeros_like(good, dtype=torch.bool)
+    hit[0, 0, 5] = hit[1, 0, 29] = True
+    assert torch.isnan(bad[hit]).all() and torch.equal(bad[~hit], good[~hit])
+
+
 def test_decode_shared_prefix_pages():
     lens = [100, 90, 64]
     table, pool = table_for(lens, 32, 3, shared=2)
