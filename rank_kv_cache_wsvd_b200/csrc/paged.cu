@@ -697,9 +697,10 @@ struct Queries16 {
   }
 };
 
-// Strips that a segment's fixed cost counts as.  Measured (a ragged batch with
-// four tokens a sequence, 0 / 8 / 16 / 24 strips): 33.9 / 26.3 / 25.6 / 25.9 us; 32
-// heads of 1600 rows 12.4 / 11.7 / 10.6 / 10.6 us.
+// Strips that a segment's fixed cost counts as.  Measured, 0 / 8 / 16 / 24 / 32 / 48 strips
+// in us: nine ragged sequences with 28 queries of 4 heads of 64 24.0 / 22.1 / 21.5 / 20.8 /
+// 20.6 / 21.2; with 7 queries 16.0 / 15.4 / 14.5 / 13.3 / 13.6 / 13.6; 32 heads of 1600 rows
+// 13.3 / 14.0 / 11.8 / 11.1 / 11.2 / 11.3.
 constexpr int kLead = 24;
 
 // Up to 8 queries a head, many units and sequences of few strips: every warp is a
