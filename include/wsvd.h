@@ -104,12 +104,17 @@ size_t dense_cache_bytes(int B, int H, int L_cap, int Hd);
  *   out       [B][H][Hd]     float32, written.
  *   workspace                device scratch of at least
  *                            wsvd_decode_workspace_size(B, H, r) bytes that is
- *                            ZERO before the first call (cudaMemset once):
- *                            it holds split partials, one completion counter
- *                            per (b, h) and the projected queries q' [B][H][r]
- *                            fp32, and every call leaves the counters zero.
- *                            Calls that share a workspace must not overlap on
- *                            the GPU.
+ *                            ZERO before the first call (cudaMemset once): it
+ *                            holds 8 KB of completion counters, split partials
+ *                            and the projected queries q' [B][H][r] fp32.
+ *                            Every call leaves the counters zero, and their
+ *                            place does not depend on the sizes, so one buffer
+ *                            that is large enough serves calls of any sizes in
+ *                            turn: of this call, of its forms below (int8
+ *                            weights, one step, paged), of the comparison
+ *                            decodes.  The other calls have workspaces of
+ *                            their own.  Calls that share a workspace must
+ *                            not overlap on the GPU.
  *   err                      optional device int32; WSVD_DEVERR_LEN_RANGE.
  * Rows >= seq_lens[b] are never used: their bytes may hold anything.
  * Depending on the sizes, one call launches one kernel (one cluster of CTAs
@@ -176,8 +181,8 @@ int wsvd_decode_gqa(int B, int Hq, int Hkv, int Hd, int r, int bits, int L_cap, 
  * pre-sized pool owned by another allocator, code that runs where a device
  * allocation would synchronise the device or fail (inside latency-critical
  * loops, under memory limits), or a host language binding without access to
- * device allocation.  The scratch it needs (split partials and one counter
- * per (b, h), the projected queries) lives in a static device array of WSVD_NOALLOC_SCRATCH_BYTES
+ * device allocation.  The scratch it needs (counters, split partials, the
+ * projected queries) lives in a static device array of WSVD_NOALLOC_SCRATCH_BYTES
  * that every GPU loading the library holds until the process exits; the call
  * itself allocates nothing.
  *   - A problem whose scratch need, wsvd_decode_workspace_size(B, H, r),
@@ -188,8 +193,8 @@ int wsvd_decode_gqa(int B, int Hq, int Hkv, int Hd, int r, int bits, int L_cap, 
  *     that first call before any stream capture.
  *   - Arguments are validated as by wsvd_decode_attention, in the same
  *     order, before anything is queued on `stream`; then the call clears the
- *     per-(b, h) counters (an asynchronous memset of 4 * B * H bytes on
- *     `stream`) and launches the decode.
+ *     counters (an asynchronous memset of 8 KB on `stream`) and launches the
+ *     decode.
  *   - All calls share the one array: calls that overlap on the GPU (other
  *     streams, other threads) race and give wrong results.                  */
 #define WSVD_NOALLOC_SCRATCH_BYTES (2u << 20)
@@ -562,8 +567,8 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  * against the weights p_l * s_V,l in 22-bit fixed point relative to the largest
  * of 32 to 128 rows.
  *   workspace  as for wsvd_decode_attention (wsvd_decode_workspace_size(B, H, r)
- *              bytes, ZERO before the first call); calls of the two may use one
- *              in turn.
+ *              bytes, ZERO before the first call); calls of the two, of any
+ *              sizes, may use one in turn.
  *   err        optional; WSVD_DEVERR_LEN_RANGE for seq_lens[b] < 0 or
  *              > max_pages * page_size (that sequence's output is 0),
  *              WSVD_DEVERR_PAGE_RANGE for a bad page (that sequence's output is

@@ -24,23 +24,23 @@ inline float resolve_scale(float softmax_scale, int Hd) {
 
 inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 
-// Decode workspace: split partials (m, l, o[W]) for every slot a persistent
-// grid can use, one completion counter per (b, h), then the projected query
-// q' [B][H][W] fp32 of the persistent path.
-inline size_t partial_bytes(int B, int H, int W) {
-  return align16(((size_t)kMaxDecodeCtas + (size_t)B * H) * ((size_t)W + 2) * sizeof(float));
+// Decode workspace: the completion counters, then split partials (m, l, o[W]) for
+// every slot a persistent grid can use, and at its end the projected query q'
+// [B][H][W] fp32 of the persistent path.
+inline size_t query_offset(int B, int H, int W) {
+  return align16(((size_t)kWorkspaceSlots + (size_t)B * H) * ((size_t)W + 2) * sizeof(float)) +
+         align16((size_t)B * H * 4);
 }
-inline size_t counter_bytes(int B, int H) { return align16((size_t)B * H * 4); }
 inline size_t decode_ws_bytes(int B, int H, int W) {
-  return partial_bytes(B, H, W) + counter_bytes(B, H) + align16((size_t)B * H * W * sizeof(float));
+  return query_offset(B, H, W) + align16((size_t)B * H * W * sizeof(float));
 }
 
 // Carve the caller's decode workspace into the kernel's regions.
 void bind_workspace(DecodeArgs* a, void* workspace) {
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  a->partials = reinterpret_cast<float*>(w);
-  a->counters = reinterpret_cast<int32_t*>(w + partial_bytes(a->B, a->H, a->W));
-  a->qglobal = reinterpret_cast<float*>(w + partial_bytes(a->B, a->H, a->W) + counter_bytes(a->B, a->H));
+  a->counters = reinterpret_cast<int32_t*>(w);
+  a->partials = reinterpret_cast<float*>(w + kSplitCounterBytes);
+  a->qglobal = reinterpret_cast<float*>(w + query_offset(a->B, a->H, a->W));
 }
 
 // Device address of pinned host memory that is mapped into the device's
@@ -198,9 +198,7 @@ int wsvd::decode_with_scratch(int B, int H, int Hd, int r, int bits, int L_cap, 
   if (st != WSVD_OK || B == 0) return st;
   // Only the counters must start at zero: partials and q' are written before
   // they are read.
-  if (cudaMemsetAsync(static_cast<uint8_t*>(scratch) + partial_bytes(B, H, r), 0, counter_bytes(B, H), stream) !=
-      cudaSuccess)
-    return WSVD_ERR_CUDA;
+  if (cudaMemsetAsync(scratch, 0, kSplitCounterBytes, stream) != cudaSuccess) return WSVD_ERR_CUDA;
   return run_decode(bits == 8 ? kCodecI8 : kCodecI4, r * bits / 8, kQProj, a, scratch, stream);
 }
 

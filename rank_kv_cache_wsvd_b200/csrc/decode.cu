@@ -24,7 +24,8 @@
 // CTAs, so ragged lengths cost nothing extra.  A CTA that owns all tiles of a
 // (b, h) finishes it alone; otherwise each CTA writes one partial (m, l,
 // o[W]) into slot c + b*H + h (slots of consecutive CTAs never collide because
-// tile ranges are ordered) and bumps a per-(b, h) counter; the CTA that
+// tile ranges are ordered) and bumps the counter of the first CTA that holds
+// part of it (a CTA is that for one (b, h) at most); the CTA that
 // arrives last merges the partials and applies B_Vh (last-arriver pattern, no
 // waiting), then resets the counter to zero.
 //
@@ -1072,7 +1073,7 @@ __global__ void __launch_bounds__(kPersistThreads, 2) decode_kernel(const Decode
         __threadfence();  // publish before the counter bump
         __syncwarp();
         int prev = 0;
-        if (lane == 0) prev = atomicAdd(&a.counters[bh], 1);
+        if (lane == 0) prev = atomicAdd(&a.counters[cf], 1);
         prev = __shfl_sync(0xffffffffu, prev, 0);
         if (prev == cl - cf) {  // last arriver: merge every partial of (b, h) in CTA order
           __threadfence();
@@ -1083,7 +1084,7 @@ __global__ void __launch_bounds__(kPersistThreads, 2) decode_kernel(const Decode
           for (int e = lane; e < W + 1; e += 32) mres[1 + e] = merge_elem<W, true>(part, np, M, e);
           __syncwarp();
           helper_finalize<W>(mres, Bvh, outp, a.Hd, lane);
-          if (lane == 0) atomicExch(&a.counters[bh], 0);
+          if (lane == 0) atomicExch(&a.counters[cf], 0);
         }
       }
       __syncwarp();
@@ -1127,7 +1128,7 @@ __global__ void __launch_bounds__(kPersistThreads, 2) decode_kernel(const Decode
     // publishing or bumping anything itself.  The read is issued before the
     // reduction so that its latency overlaps it (an early, lower count only
     // sends this CTA down the publishing path).
-    const int seen = (cf != cl && tid == 0) ? ld_acquire_gpu(&a.counters[bh]) : 0;
+    const int seen = (cf != cl && tid == 0) ? ld_acquire_gpu(&a.counters[cf]) : 0;
     reduce_to_res<VPT, TPT, W, C::kNSeg>(m, l, acc, red, res, tid);
     float* outp = a.out + ((size_t)b_ * a.H + h_) * a.Hd;
     BvRef Bvh{nullptr, a.w8, a.w8 ? a.sBv + (size_t)h_ * a.Hd : nullptr};
@@ -1156,7 +1157,7 @@ __global__ void __launch_bounds__(kPersistThreads, 2) decode_kernel(const Decode
     csync();
     if (!early) {
       if (tid == 0) {
-        const int prev = atomicAdd(&a.counters[bh], 1);
+        const int prev = atomicAdd(&a.counters[cf], 1);
         *flag = (prev == cl - cf) ? 1 : 0;
       }
       csync();
@@ -1164,7 +1165,7 @@ __global__ void __launch_bounds__(kPersistThreads, 2) decode_kernel(const Decode
     if (*flag) {
       if (!early) __threadfence();
       merge_rows<W, true>(a.partials + ((size_t)cf + bh) * (W + 2), cl - cf + 1, res, tid);
-      if (tid == 0) atomicExch(&a.counters[bh], 0);
+      if (tid == 0) atomicExch(&a.counters[cf], 0);
       finalize_out<W>(res, Bvh, outp, a.Hd, red, tid);
     }
   };

@@ -1,4 +1,4 @@
-// Decode entry point that allocates nothing: the split partials and per-(b, h)
+// Decode entry point that allocates nothing: the split partials and the
 // completion counters live in a file-scope device array instead of a caller
 // workspace.  For callers that cannot call cudaMalloc (see wsvd.h).
 #include <map>

@@ -75,7 +75,7 @@ struct LatDecodeArgs {
   const __half *Bk, *Bv; // [H][r][Hd]
   float* out;
   float* partials;       // [kMaxDecodeCtas + B * H][r + 2]: o, then m, l
-  int32_t* counters;
+  int32_t* counters;     // [kMaxDecodeCtas], by the first worker of a cut head
   int32_t* err;
   float qscale;
 };
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
       __threadfence();
       __syncwarp();
       int last = 0;
-      if (lane == 0) last = atom_add_acq_rel_gpu(a.counters + bh, 1) == np - 1;
+      if (lane == 0) last = atom_add_acq_rel_gpu(a.counters + wf, 1) == np - 1;
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
       __threadfence();
       const float* from = a.partials + ((size_t)wf + bh) * kSlot;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
         }
         m = mx;
       }
-      if (lane == 0) st_relaxed_gpu(a.counters + bh, 0);
+      if (lane == 0) st_relaxed_gpu(a.counters + wf, 0);
 #pragma unroll
       for (int k = 0; k < NJ; ++k)
         if (k * 32 + lane < R) sm_q[warp][k * 32 + lane] = sum[k];
@@ -582,7 +582,6 @@ bool pick_lat(int bits, int rowbytes, LatKernel* k) {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 
 // Bytes in front of the prefill's scratch in the paged append's workspace: the
 // one-token append's completion counter, which every call leaves zero.
@@ -618,9 +617,8 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   if (!aligned16(q) || !aligned16(lat_k) || !aligned16(lat_v) || !aligned16(scale_k) || !aligned16(scale_v) ||
       !aligned16(B_k) || !aligned16(B_v) || !aligned16(out) || !aligned16(workspace))
     return WSVD_ERR_INVALID_ARG;
-  // The workspace of wsvd_decode_attention, laid out for this kernel: the
-  // counters where that call has them, so that calls of both may use it in turn.
-  const size_t counters = align16(((size_t)kMaxDecodeCtas + (size_t)B * H) * ((size_t)r + 2) * sizeof(float));
+  // The workspace of wsvd_decode_attention: the counters where that call has
+  // them, so that calls of both, of any sizes, may use it in turn.
   if (workspace_bytes < wsvd_decode_workspace_size(B, H, r)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   LatDecodeArgs a{};
@@ -631,8 +629,8 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
   a.scale_k = static_cast<const __half*>(scale_k); a.scale_v = static_cast<const __half*>(scale_v);
   a.Bv = static_cast<const __half*>(B_v);
   a.out = out;
-  a.partials = reinterpret_cast<float*>(w);
-  a.counters = reinterpret_cast<int32_t*>(w + counters);
+  a.counters = reinterpret_cast<int32_t*>(w);
+  a.partials = reinterpret_cast<float*>(w + kSplitCounterBytes);
   a.q = static_cast<const uint16_t*>(q);
   a.q_dtype = q_dtype;
   a.Bk = static_cast<const __half*>(B_k);

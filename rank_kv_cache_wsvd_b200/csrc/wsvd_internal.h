@@ -18,8 +18,19 @@ constexpr int kConsumerWarps = 8;
 constexpr int kConsumerThreads = kConsumerWarps * 32;
 constexpr int kDecodeThreads = kConsumerThreads + 32;   // cluster kernel: + producer warp
 constexpr int kPersistThreads = kConsumerThreads + 64;  // persistent kernel: + producer and helper warps
-// Upper bound on the persistent grid; sizes the partial-result workspace.
-constexpr int kMaxDecodeCtas = 2048;
+// A decode's workspace begins with its completion counters, one per worker (CTA or
+// warp): a (b, h) cut over several workers is counted at the first of them, which is
+// the first of no other.  They lie in front of the partial results, whose extent
+// depends on the call's sizes, so that no call writes where another has its
+// counters: one zeroed buffer serves calls of any sizes in turn.
+constexpr size_t kSplitCounterBytes = 8192;
+// Workers a decode may have.  The workspace's size is that of kWorkspaceSlots
+// partial results; the slots past kMaxDecodeCtas make room for the counters.
+constexpr int kWorkspaceSlots = 2048, kMaxDecodeCtas = 1920;
+constexpr int kMinDecodeWidth = 16;  // of a latent row (16 bytes of int8)
+static_assert(kMaxDecodeCtas * sizeof(int32_t) <= kSplitCounterBytes &&
+                  (kWorkspaceSlots - kMaxDecodeCtas) * (kMinDecodeWidth + 2) * sizeof(float) >= kSplitCounterBytes,
+              "the counters take the place of partial results that no worker has");
 
 enum Codec { kCodecI8 = 0, kCodecI4 = 1, kCodecF16 = 2 };
 enum QMode { kQProj = 0, kQDirect = 1, kQGlobal = 2 };
@@ -47,7 +58,7 @@ struct DecodeArgs {
   float qscale;          // softmax_scale * log2(e)
   float* out;            // [B][H][Hd]
   float* partials;       // [(kMaxDecodeCtas + B*H)][W + 2]
-  int32_t* counters;     // [B*H], zero between calls
+  int32_t* counters;     // [kMaxDecodeCtas], by the first CTA of a cut (b, h); zero between calls
   int32_t* err;
 };
 
@@ -89,8 +100,8 @@ struct AppendArgs {
 int append_cluster_size(int E, int blk);
 // wsvd_decode_attention with caller-provided scratch that is NOT zero on entry
 // (the no-allocation entry point's static array): validates every argument
-// exactly as wsvd_decode_attention does, and only then clears the per-(b, h)
-// counters (an asynchronous memset on `stream`) and launches.  Nothing is
+// exactly as wsvd_decode_attention does, and only then clears the counters (an
+// asynchronous memset on `stream`) and launches.  Nothing is
 // queued when validation fails.
 int decode_with_scratch(int B, int H, int Hd, int r, int bits, int L_cap, const int32_t* seq_lens, const void* q,
                         int q_dtype, const uint8_t* lat_k, const uint8_t* lat_v, const void* scale_k,
