@@ -112,7 +112,7 @@ size_t dense_cache_bytes(int B, int H, int L_cap, int Hd);
  *                            that is large enough serves calls of any sizes in
  *                            turn: of this call, of its forms below (int8
  *                            weights, one step, paged), of the comparison
- *                            decodes.  The other calls have workspaces of
+ *                            decodes and of paged_decode_attention.  The other calls have workspaces of
  *                            their own.  Calls that share a workspace must
  *                            not overlap on the GPU.
  *   err                      optional device int32; WSVD_DEVERR_LEN_RANGE.
@@ -518,9 +518,10 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
  *   softmax_scale 0 selects 1/sqrt(Hd).
  *   Hq a multiple of Hkv; Hq / Hkv * Tq <= 64.
  *   workspace at least paged_decode_workspace_size(...) bytes, ZERO before the
- *             first call (split partials, one counter per sequence, head and
- *             group of 8 or 16 queries; every call leaves the counters zero).
- *             Calls sharing it must not overlap on the GPU.
+ *             first call: counters and split partials as in the workspace of
+ *             wsvd_decode_attention.  One buffer that is large enough serves
+ *             calls of any sizes, and those decodes, in turn.  Calls sharing
+ *             it must not overlap on the GPU.
  *   err       optional; WSVD_DEVERR_LEN_RANGE for seq_lens[b] < 0 or
  *             > max_pages * page_size (that sequence's output is 0),
  *             WSVD_DEVERR_PAGE_RANGE for a bad page (that sequence's output is

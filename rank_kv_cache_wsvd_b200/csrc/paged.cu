@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "paged.cuh"
+#include "wsvd_internal.h"
 
 using namespace wsvd;
 
@@ -270,7 +271,7 @@ struct KvDecodeArgs {
   const uint16_t *q, *k, *v;
   float* out;
   float* partials;  // two a worker: O [min(nq, kQ)][HD], then (m, l) per query
-  int32_t* counters;
+  int32_t* counters;  // by the first worker of a cut unit
   int32_t* err;
   float qscale;
 };
@@ -712,7 +713,7 @@ constexpr int kLead = 24;
 // with 8 queries 64 x 300 28.4 / 30.0; one sequence of 300 rows, whose few units warps
 // would have to join, 7.8 / 15.
 constexpr int kSoloStrips = 40, kSoloUnits = 512, kSoloLead = 4;
-constexpr int kMaxSolo = 2048;  // workers that way at most; sizes the partials
+constexpr int kMaxSolo = 2016;  // workers that way at most
 
 // MANY: many units, so that their sequences may be short (kSoloUnits); a kernel of
 // its own, as the code alone costs a small call half a microsecond.
@@ -828,7 +829,6 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
     const int slot = partial_floats(qmax, HD);
     // A worker has at most one unit that it begins within, and one that it only begins.
     float* part = a.partials + (size_t)(2 * me + (seg.s == 0 ? 1 : 0)) * slot;
-    const size_t unit = (size_t)seg.b * seqs.units + seg.u;
     auto store = [&](int j, int d, float4 v, float L) {
       const int jq = j0 + j, t = jq / a.G;
       const float f = lim_min + t > 0 ? 1.f / L : 0.f;
@@ -902,11 +902,11 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
       share.holders(seg, &wf, &np);
       __threadfence();
       __syncwarp();
-      if (lane == 0) last = atom_add_acq_rel_gpu(a.counters + unit, 1) == np - 1;
+      if (lane == 0) last = atom_add_acq_rel_gpu(a.counters + wf, 1) == np - 1;
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
       __threadfence();
       join(lane, 32);
-      if (lane == 0) st_relaxed_gpu(a.counters + unit, 0);
+      if (lane == 0) st_relaxed_gpu(a.counters + wf, 0);
       continue;
     }
 
@@ -951,12 +951,12 @@ __global__ void __launch_bounds__(DecCfg<BF16, HD, NB>::kThreads, 1) kv_decode_k
       share.holders(seg, &wf, &np);
       __threadfence();
       __syncthreads();
-      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + unit, 1) == np - 1;
+      if (tid == 0) sm_last = atom_add_acq_rel_gpu(a.counters + wf, 1) == np - 1;
       __syncthreads();
       if (sm_last) {
         __threadfence();
         join(tid, C::kThreads);
-        if (tid == 0) st_relaxed_gpu(a.counters + unit, 0);
+        if (tid == 0) st_relaxed_gpu(a.counters + wf, 0);
       }
     }
     __syncthreads();  // the scratch and the statistics are free again
@@ -997,17 +997,19 @@ DecodeKernel pick_decode(int Hd, int qc, bool many) {
   }
 }
 
-struct DecodeWs {
-  size_t partials, counters, total;
-};
-DecodeWs decode_ws(int B, int Tq, int Hq, int Hkv, int Hd) {
+// The workspace: the counters (kSplitCounterBytes, in front, so that no size of call
+// moves them), then two partial results a worker.  Its size is that of 2048 warps
+// or 592 CTAs and a counter per unit; the workers that a call never has make room
+// for the counters.
+constexpr int kSoloSlots = 2048, kCtaSlots = 592;
+static_assert(kMaxSolo * sizeof(int32_t) <= kSplitCounterBytes && kMaxPagedCtas <= kMaxSolo, "a counter a worker");
+static_assert((kSoloSlots - kMaxSolo) * 2 * partial_floats(1, 32) * sizeof(float) >= kSplitCounterBytes &&
+                  (kCtaSlots - kMaxPagedCtas) * 2 * partial_floats(9, 32) * sizeof(float) >= kSplitCounterBytes,
+              "the counters take the place of partial results that no worker has");
+size_t decode_ws(int B, int Tq, int Hq, int Hkv, int Hd) {
   const int nq = Hq / Hkv * Tq, qc = chunk_queries(nq, Hd), chunks = (nq + qc - 1) / qc;
-  DecodeWs w;
-  w.partials = 0;
-  w.counters = align16((size_t)2 * (qc == 8 ? kMaxSolo : kMaxPagedCtas) * partial_floats(std::min(nq, qc), Hd) *
-                       sizeof(float));
-  w.total = w.counters + align16((size_t)B * Hkv * chunks * sizeof(int32_t));
-  return w;
+  return align16((size_t)2 * (qc == 8 ? kSoloSlots : kCtaSlots) * partial_floats(std::min(nq, qc), Hd) * sizeof(float)) +
+         align16((size_t)B * Hkv * chunks * sizeof(int32_t));
 }
 
 }  // namespace
@@ -1110,7 +1112,7 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
 
 size_t paged_decode_workspace_size(int B, int Tq, int Hq, int Hkv, int Hd) {
   if (B < 0 || Tq < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || Hd < 1) return 0;
-  return decode_ws(B, Tq, Hq, Hkv, Hd).total;
+  return decode_ws(B, Tq, Hq, Hkv, Hd);
 }
 
 int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size, int num_pages, int max_pages,
@@ -1128,8 +1130,7 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   if (!seq_lens || !block_table || !q || !k_pages || !v_pages || !out || !workspace) return WSVD_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
     return WSVD_ERR_INVALID_ARG;
-  const DecodeWs ws = decode_ws(B, Tq, Hq, Hkv, Hd);
-  if (workspace_bytes < ws.total) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < decode_ws(B, Tq, Hq, Hkv, Hd)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
   const int qc = chunk_queries((int)nq, Hd);
   const bool many = (long long)B * Hkv * ((nq + qc - 1) / qc) >= kSoloUnits;
   const DecodeKernel kern = dtype == WSVD_DTYPE_BF16 ? pick_decode<true>(Hd, qc, many) : pick_decode<false>(Hd, qc, many);
@@ -1140,8 +1141,8 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k_pages);
   a.v = static_cast<const uint16_t*>(v_pages);
   a.out = out;
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.partials);
-  a.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + ws.counters);
+  a.counters = static_cast<int32_t*>(workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kSplitCounterBytes);
   a.err = err;
   a.qscale = (softmax_scale != 0.f ? softmax_scale : (float)(1.0 / sqrt((double)Hd))) * kLog2e;
   (void)cudaGetLastError();

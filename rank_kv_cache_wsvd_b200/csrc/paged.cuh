@@ -182,8 +182,8 @@ cudaError_t launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
-// Upper bound of the paged decodes' grids; sizes their partial results.
-constexpr int kMaxPagedCtas = 592;
+// Upper bound of the paged decodes' grids.
+constexpr int kMaxPagedCtas = 588;
 
 // log2 of a page size the paged caches take (16 .. 256), else -1.
 inline int page_shift_of(int page_size) {

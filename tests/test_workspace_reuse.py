@@ -55,6 +55,15 @@ def _dense(B, H=32, Hd=64, L_cap=256):
         q, K, V, n, out=out, workspace_buf=ws), (B, H, Hd)
 
 
+def _dense_paged(Tq, G, B=64, Hkv=8, Hd=128, lo=100, hi=600):
+    lens = _lens(B, lo, hi, 5)
+    table, pool = table_for(lens, 32, 3)
+    kp, vp = randn((pool, Hkv, 32, Hd), "bf16", 1), randn((pool, Hkv, 32, Hd), "bf16", 2)
+    q, tab, n = randn((B, Tq, G * Hkv, Hd), "bf16", Tq + G), cuda(table), cuda(np.asarray(lens, np.int32))
+    return W.paged_decode_workspace_size(B, Tq, G * Hkv, Hkv, Hd), lambda out, ws: W.paged_decode_attention(
+        q, kp, vp, tab, n, out=out, workspace_buf=ws), (B, Tq, G * Hkv, Hd)
+
+
 def _in_turn(calls, order):
     """Every call alone, then all through one buffer that is zeroed once."""
     fresh = [call(torch.full(shape, float("nan"), device="cuda"), None) for _, call, shape in calls]
@@ -75,6 +84,17 @@ def test_latent_paged_decode_of_other_ranks(bits, r):
     _in_turn([_latent_paged(9, r=r, bits=bits), _latent_paged(4), _latent_paged(3, H=7, r=r, bits=bits)], [0, 1, 2, 0, 2, 1, 0])
 
 
+@pytest.mark.parametrize("G", [4, 8])
+def test_dense_paged_decode_of_one_and_several_tokens(G):
+    _in_turn([_dense_paged(t, G) for t in (1, 2, 4)], [0, 1, 0, 2, 0, 2, 1, 0])
+
+
+def test_dense_paged_decode_of_other_head_sizes_and_batches():
+    _in_turn([_dense_paged(1, 4), _dense_paged(1, 1, B=300, Hkv=4, Hd=32, lo=1, hi=300),
+              _dense_paged(3, 4, B=3, Hkv=2, Hd=256, lo=900, hi=4000), _dense_paged(2, 16, B=5, Hkv=2, Hd=64, hi=5000)],
+             [0, 1, 2, 3, 0, 3, 1, 2, 1, 0])
+
+
 def test_latent_decode_of_a_batch_that_shrinks_and_grows():
     _in_turn([_latent(96), _latent(4, L_cap=8192), _latent(5, L_cap=8192), _latent(6, L_cap=8192), _latent(80)],
              [0, 1, 2, 3, 0, 3, 4, 2, 1, 0])
@@ -84,14 +104,14 @@ def test_dense_decode_of_a_batch_that_shrinks_and_grows():
     _in_turn([_dense(96), _dense(4, L_cap=4096), _dense(5, L_cap=4096), _dense(6, L_cap=4096)], [0, 1, 2, 3, 0, 2, 3, 1, 0])
 
 
-def test_the_contiguous_and_the_paged_decodes_share_one_workspace():
-    _in_turn([_latent_paged(16), _latent(40), _dense(40), _latent_paged(3), _latent(4, L_cap=8192)],
-             [0, 1, 2, 3, 4, 1, 0, 3, 2, 4, 0])
+def test_different_decodes_share_one_workspace():
+    _in_turn([_latent_paged(16), _dense_paged(2, 4), _latent(40), _dense(40), _latent_paged(3), _dense_paged(1, 8),
+              _latent(4, L_cap=8192)], [0, 1, 2, 3, 4, 5, 6, 2, 0, 6, 3, 1, 5, 4, 3, 0])
 
 
 def test_every_call_leaves_the_counters_zero():
     """The first 8 KB hold the counters, whatever the sizes."""
-    calls = [_latent_paged(16), _latent(40), _dense(40)]
+    calls = [_latent_paged(16), _dense_paged(2, 4), _dense_paged(1, 4), _dense_paged(4, 8), _latent(40), _dense(40)]
     ws = W.workspace(max(need for need, _, _ in calls))
     for _, call, shape in calls:
         call(torch.empty(shape, device="cuda"), ws)
