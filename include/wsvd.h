@@ -154,12 +154,15 @@ int wsvd_decode_attention(int B, int H, int Hd, int r, int bits, int L_cap, cons
  *   Hq a multiple of Hkv; G * Tq <= 64; Hd in {32, 64, 128, 256}; row bytes
  *   r*bits/8 in {16, 32, 64} (int8 r = 16, 32, 64; int4 r = 32, 64, 128);
  *   L_cap a multiple of 8; B <= 65535.  Else WSVD_ERR_UNSUPPORTED.
- *   workspace  at least wsvd_decode_multi_workspace_size(...) bytes, ZERO
- *             before the first call; it holds split partials and one counter
- *             per (sequence, latent head, group of 16 queries); every call
- *             leaves the counters zero.  Calls sharing it must not overlap.
+ *   workspace  at least wsvd_decode_multi_workspace_size(...) bytes, no
+ *             zeroing needed: it holds split partials, one counter per
+ *             (sequence, latent head, group of 16 queries) and the projected
+ *             queries, and every call clears its counters itself.  One buffer
+ *             serves calls of any sizes in turn, but not those calls that
+ *             expect to find theirs zero.  Calls sharing it must not overlap.
  *   err        optional; WSVD_DEVERR_LEN_RANGE as for wsvd_decode_attention.
- * One launch per call.                                                       */
+ * Two launches: the queries' projection, and the decode behind it as its
+ * programmatic dependent.                                                    */
 size_t wsvd_decode_multi_workspace_size(int B, int Tq, int Hq, int Hkv, int r, int L_cap);
 int wsvd_decode_multi(int B, int Tq, int Hq, int Hkv, int Hd, int r, int bits, int L_cap, const int32_t* seq_lens,
                       const void* q, int q_dtype, const uint8_t* lat_k, const uint8_t* lat_v, const void* scale_k,

@@ -70,7 +70,7 @@ struct GroupedArgs {
   float* out;        // [B][Tq][Hq][Hd]
   const uint8_t* qplanes;  // [B * Hkv * nqc] blocks of the q' planes (score operand layout) + steps
   float* partials;   // [B * Hkv * nqc][slot_stride][NQ][r + 2]
-  int32_t* counters; // [B * Hkv * nqc], zero between calls
+  int32_t* counters; // [B * Hkv * nqc], zeroed by the projection
   int32_t* err;
 };
 
@@ -238,6 +238,10 @@ __global__ void __launch_bounds__(128) grouped_qproj_kernel(const GroupedArgs a,
   const int grp = blockIdx.x, t = threadIdx.x;
   const int qc = grp % a.nqc, hkv = (grp / a.nqc) % a.Hkv, b = grp / (a.nqc * a.Hkv);
   const int nq = min(NQ, a.G * a.Tq - qc * NQ);
+  // The group's counter: its place depends on the call's sizes, so what a call of
+  // others left there is cleared here.  The decode grid counts only what the planes
+  // below went into, after this grid has completed.
+  if (t == 0) a.counters[grp] = 0;
   {
     const uint4* src = reinterpret_cast<const uint4*>(a.Bk + (size_t)hkv * R * a.Hd);
     uint4* dst = reinterpret_cast<uint4*>(bks);
@@ -717,7 +721,6 @@ __global__ void __launch_bounds__(kGThreads, 2) grouped_decode_kernel(const Grou
           res[ql * (R + 2) + col] = acc2;
         }
         named_barrier_sync(1, kGConsumers);
-        if (ct == 0) atomicExch(&a.counters[gidx], 0);
       }
     }
     if (finish) {  // out_q = (O_q / l_q) . B_Vh

@@ -55,6 +55,14 @@ def _dense(B, H=32, Hd=64, L_cap=256):
         q, K, V, n, out=out, workspace_buf=ws), (B, H, Hd)
 
 
+def _grouped(B, Tq=1, Hq=32, Hkv=8, r=32, bits=8, Hd=64, L_cap=2048):
+    lk, lv, sk, sv = _codes((B, Hkv, L_cap), r, bits, B)
+    Bk, Bv = (randn((Hkv, r, Hd), "fp16", s) * r ** -0.5 for s in (1, 2))
+    q, n = randn((B, Tq, Hq, Hd), "fp16", B), cuda(np.asarray(_lens(B, L_cap // 2, L_cap, B), np.int32))
+    return W.wsvd_decode_multi_workspace_size(B, Tq, Hq, Hkv, r, L_cap), lambda out, ws: W.wsvd_decode_multi(
+        q, lk, lv, sk, sv, Bk, Bv, n, bits, out=out, workspace_buf=ws), (B, Tq, Hq, Hd)
+
+
 def _dense_paged(Tq, G, B=64, Hkv=8, Hd=128, lo=100, hi=600):
     lens = _lens(B, lo, hi, 5)
     table, pool = table_for(lens, 32, 3)
@@ -102,6 +110,18 @@ def test_latent_decode_of_a_batch_that_shrinks_and_grows():
 
 def test_dense_decode_of_a_batch_that_shrinks_and_grows():
     _in_turn([_dense(96), _dense(4, L_cap=4096), _dense(5, L_cap=4096), _dense(6, L_cap=4096)], [0, 1, 2, 3, 0, 2, 3, 1, 0])
+
+
+def test_grouped_decode_of_other_batches_and_tokens():
+    _in_turn([_grouped(8), _grouped(3), _grouped(2, Tq=4), _grouped(5, Hq=8, L_cap=4096)], [0, 1, 2, 3, 0, 3, 1, 2, 0])
+
+
+def test_grouped_decode_needs_no_zeroed_workspace():
+    need, call, shape = _grouped(4)
+    want = call(torch.full(shape, float("nan"), device="cuda"), None)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(call(torch.full(shape, float("nan"), device="cuda"), ws), want)
 
 
 def test_different_decodes_share_one_workspace():
