@@ -216,6 +216,9 @@ int wsvd_decode_attention_noalloc(int B, int H, int Hd, int r, int bits, int L_c
  *   code_j = clamp(round_half_even(c_j / scale), -Q, Q) (scale 0 -> codes 0);
  *   row seq_lens[b] of lat_k/lat_v/scale_k/scale_v is written, then
  *   seq_lens[b] += 1.
+ * Latents that are not finite, or too large for an fp16 scale, give an
+ * infinite or NaN scale, which a decode that reads the row carries to its
+ * output; this holds for every append and prefill below.
  * A sequence with seq_lens[b] >= L_cap (or < 0) is not written and not
  * advanced; WSVD_DEVERR_CACHE_FULL is raised.
  *

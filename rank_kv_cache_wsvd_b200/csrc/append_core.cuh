@@ -282,11 +282,11 @@ __device__ __forceinline__ __half quantise_append_row(const float* slots, size_t
         if (q < nranks) sum += slots[(size_t)q * stride + j];
       cv[k] = sum * hnorm;
       if (W8) cv[k] *= cs.v[k];  // column scale of int8 A
-      amax = fmaxf(amax, fabsf(cv[k]));
+      amax = max_abs(amax, cv[k]);
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 16; o > 0; o >>= 1) amax = max_abs(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
   const float sc = __half2float(sh);
 #pragma unroll

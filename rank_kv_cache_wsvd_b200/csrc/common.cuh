@@ -197,6 +197,12 @@ __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The larger of amax and |x|, as integers: a NaN lies above infinity and stays,
+// where fmaxf drops it.  For the largest latent of a row, whose scale then is NaN.
+__device__ __forceinline__ float max_abs(float amax, float x) {
+  return __int_as_float(max(__float_as_int(amax), __float_as_int(fabsf(x))));
+}
+
 // gpu-scope acquire load (a completion counter that other CTAs bump after a
 // release of their data).
 __device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {

@@ -376,10 +376,10 @@ __global__ void __launch_bounds__(BlockCfg<R, BN_, TOK_>::kThreads, 1)
     for (int c = 0; c < QCOLS / 4; ++c) {
       const float4 x = src[c];
       v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
-      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+      amax = max_abs(max_abs(max_abs(max_abs(amax, x.x), x.y), x.z), x.w);
     }
 #pragma unroll
-    for (int o = LPU / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = LPU / 2; o > 0; o >>= 1) amax = max_abs(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (!real) continue;
     const int b = m / a.T, t = m - b * a.T, pos = sm_pos[r0 + row], why = sm_why[r0 + row];
     if (why) {

@@ -451,10 +451,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prefill_gemm_kernel(const Pre
     for (int q = 0; q < 4; ++q) {
       const int j = lane + 32 * q;
       cv[q] = j < a.r ? cs[i * kCStride + hh * a.r + j] * ip : 0.f;
-      amax = fmaxf(amax, fabsf(cv[q]));
+      amax = max_abs(amax, cv[q]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = 16; o > 0; o >>= 1) amax = max_abs(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
     const float sc = __half2float(sh);
     const size_t row = ((size_t)b * a.H + h) * a.L_cap + pos + t;
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int j = 0; j < R; ++j) {
             tot[hb * R + j] *= ip;
-            amax = fmaxf(amax, fabsf(tot[hb * R + j]));
+            amax = max_abs(amax, tot[hb * R + j]);
           }
           const __half sh = __float2half_rn(__fdiv_rn(amax, (float)Q));
           const float sc = __half2float(sh);
