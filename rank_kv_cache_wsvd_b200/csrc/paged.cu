@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArg
 
   if (t < a.T) {
     const bool stored = t < there;
-    const int l = pos + t;
+    const int l = stored ? pos + t : 0;
     float4 c[2], s[2];
     size_t page_row = 0;  // of head 0; a head further lies a page further
     if (stored) {
@@ -401,7 +401,7 @@ struct Queries8 {
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[t][i] = (sc[t][i] + sc2[t][i]) * scale;
-    const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
+    const bool masked = l0 > lim_min - TS || valid != (1 << MT) - 1;
     if (masked) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -577,7 +577,7 @@ struct Queries16 {
           else mma16816<BF16>(sc[2 * t + x], q[k], f[2 * x], f[2 * x + 1]);
         }
       }
-    const bool masked = l0 + TS > lim_min || valid != (1 << MT) - 1;
+    const bool masked = l0 > lim_min - TS || valid != (1 << MT) - 1;
     if (masked) {
 #pragma unroll
       for (int t = 0; t < 2 * MT; ++t)

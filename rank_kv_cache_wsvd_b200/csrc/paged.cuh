@@ -26,13 +26,15 @@ struct PagedSeqs {
 // sequences would finish last.
 template <int TS>
 struct Strips {
+  // Unsigned: a length may be as large as an int holds.
+  static __device__ __forceinline__ int strips_of(int n) { return (int)(((uint32_t)n + (TS - 1)) / TS); }
   // A worker's share of one unit: strips [s, e) of unit u of sequence b (n
   // rows); none when the share ends within the lead.
   struct Segment {
     int b, u, n, s, e, lead;
     int at, taken;   // where the share begins in the unit (lead included), and how much of the unit it takes
     long long left;  // of the worker's share from here on
-    __device__ __forceinline__ int strips() const { return (n + TS - 1) / TS; }
+    __device__ __forceinline__ int strips() const { return strips_of(n); }
     __device__ __forceinline__ void enter(int place) {
       at = place;
       taken = (int)min((long long)(strips() + lead - at), left);
@@ -51,8 +53,6 @@ struct Strips {
       return true;
     }
   };
-
-  static __device__ __forceinline__ int strips_of(int n) { return (n + TS - 1) / TS; }
 
   long long total, base, extra, end;  // strips in all; per worker; workers with one more; this worker's end
   int workers;                        // workers that have a share

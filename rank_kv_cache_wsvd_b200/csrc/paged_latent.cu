@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
       ls = ld.s;
     }
     if (more) {
-      const int l = ls * TS + lane * 16;
+      const int l = ls * TS + lane % C::kGroups * 16;
       pg = lane < C::kGroups && l < ld.n ? __ldg(a.block_table + (size_t)ld.b * a.max_pages + (l >> a.page_shift)) : -1;
     }
   };
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(LatCfg<BITS, RB>::kThreads, 1) lat_decode_kern
       issue(stage == 0 ? S - 1 : stage - 1);
       const uint32_t kb = my_ring + (uint32_t)stage * C::kStage, vb = kb + C::kHalf, sb = vb + C::kHalf;
       const int valid = sm_valid[warp][stage];
-      const bool masked = s * TS + TS > seg.n || valid != (1 << C::kGroups) - 1;
+      const bool masked = s * TS > seg.n - TS || valid != (1 << C::kGroups) - 1;
 
       // ---- scores: lane `lane` ends with row tok of every block
       float sc[NBL];

@@ -235,3 +235,16 @@ def test_an_allowance_catches_planted_mistakes():
     rounded = ref.copy()
     rounded[0, 0, 0] = p16 @ Vr / p.sum()
     assert off(rounded) > 1
+
+
+@pytest.mark.parametrize("TS", [16, 32, 64, 128])
+def test_strips_of_lengths_at_the_end_of_the_range(TS):
+    """The decodes' 32-bit sums: strips of a length as large as an int holds, and
+    which strips look at their rows' limits (s TS > n - TS, not s TS + TS > n)."""
+    wrap = lambda x: (x + 2 ** 31) % 2 ** 32 - 2 ** 31
+    for n in (1, TS - 1, TS, TS + 1, 2 ** 31 - TS, 2 ** 31 - TS + 1, 2 ** 31 - 16, 2 ** 31 - 1):
+        strips = wrap(((n + TS - 1) % 2 ** 32) // TS)
+        assert strips == -(-n // TS)
+        s = strips - 1
+        assert (wrap(s * TS) > wrap(n - TS)) == (n % TS != 0)
+        assert all(wrap(s * TS + i) == s * TS + i for i in (0, TS - 16, TS - 1))
