@@ -552,8 +552,9 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
  * the new lengths (fp16 factors).
  *   r and bits as for wsvd_decode_attention_paged (rows of 16 to 128 bytes for
  *   int8, 16 to 64 for int4); hadamard_block a power of two in [1, 1024] that
- *   divides E; E a multiple of 64 up to 16384, and B * T <= 2^24.  One token of
- *   up to 16 sequences may also have another E that wsvd_latent_append takes.
+ *   divides E; E a multiple of 64 up to 16384, B * T <= 2^24, H * r <= 2^21 and
+ *   B * T * H * r <= 2^42.  One token of up to 16 sequences may also have another
+ *   E that wsvd_latent_append takes.
  *   One token of a few sequences (B <= 4 and B * r <= 192, or such an E) takes
  *   that call's kernel and gives its codes and scales bit for bit.  Everything
  *   else runs on the tensor cores with wsvd_latent_prefill's precision (x in

@@ -596,6 +596,7 @@ size_t paged_block_scratch(int B, int T, int E) {
 bool paged_block_takes(int B, int T, int H, int E, int r) {
   const long long M = (long long)B * T;
   return E % 64 == 0 && E <= 16384 && M <= (1LL << 24) && (long long)H * r <= (1LL << 21) &&
+         M * H * r <= (1LL << 42) &&  // tiles in an int
          (r == 16 || r == 32 || r == 64 || r == 128);
 }
 

@@ -237,6 +237,12 @@ def test_an_allowance_catches_planted_mistakes():
     assert off(rounded) > 1
 
 
+def test_latent_append_refuses_blocks_of_too_many_tiles(lib):
+    """B * T * H * r past 2^42, each within its own limit."""
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(B=1 << 12, T=1 << 12, H=1 << 14, E=64, blk=64)) == 2
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(B=1 << 12, T=1 << 12, H=1 << 13, E=64, blk=64)) == 4  # the workspace
+
+
 @pytest.mark.parametrize("TS", [16, 32, 64, 128])
 def test_strips_of_lengths_at_the_end_of_the_range(TS):
     """The decodes' 32-bit sums: strips of a length as large as an int holds, and
