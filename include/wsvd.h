@@ -500,8 +500,9 @@ int shared_latent_svd_decode(int B, int H, int Hd, int R, int L_cap, const int32
  *   workspace at least paged_kv_append_workspace_size(B) bytes, ZERO before the
  *             first call; every call leaves it zero.  Calls sharing it must not
  *             overlap.
- * What is written must not share memory with what is read or with other
- * outputs, the two in-place cases apart (else WSVD_ERR_INVALID_ARG).
+ * What a call over pages writes (workspace and err included) must not share
+ * memory with what it reads or with its other outputs, the in-place cases
+ * apart (else WSVD_ERR_INVALID_ARG); this holds for all four calls.
  * T = 0 only copies the lengths.  One launch.                               */
 size_t paged_kv_append_workspace_size(int B);
 int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int interleaved, int page_size, int num_pages,

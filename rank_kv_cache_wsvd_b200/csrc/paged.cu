@@ -1064,25 +1064,24 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
     return WSVD_ERR_INVALID_ARG;
   // Nothing that is written may share a byte with what is read, but for the
   // two that may be updated in place: the lengths, and a dense q.
-  const size_t tok = (size_t)B * T, pool = ((size_t)num_pages * Hkv << shift) * Hd * 2;
-  auto span = [&](long long stride, int heads) {
-    return tok && heads ? ((tok - 1) * (size_t)stride + (size_t)heads * Hd) * 2 : 0;
+  const size_t tok = (size_t)B * T, lb = (size_t)B * 4;
+  size_t pool;
+  if (!pool_bytes(num_pages, Hkv, shift, (size_t)Hd * 2, &pool)) return WSVD_ERR_UNSUPPORTED;
+  bool wide = false;  // a stride whose last token lies past any address
+  auto span = [&](const void* p, long long stride, int heads) {
+    size_t n = 0;
+    if (tok && heads)
+      wide |= __builtin_mul_overflow(tok - 1, (size_t)stride, &n) || __builtin_add_overflow(n, (size_t)heads * Hd, &n) ||
+              __builtin_mul_overflow(n, (size_t)2, &n);
+    return Span{p, n};
   };
-  const size_t kb = span(k_stride, Hkv), vb = span(v_stride, Hkv), qb = span(q_stride, Hq), ob = tok * Hq * Hd * 2;
-  const size_t tb = (size_t)B * max_pages * 4, cb = (size_t)max_pos * rot_dim * 4, lb = (size_t)B * 4;
-  const bool q_in_place = q_out == q && q_stride == (long long)Hq * Hd;
-  struct Span { const void* p; size_t n; } written[] = {{k_pages, pool}, {v_pages, pool}, {q_out, ob}, {seq_lens_out, lb}};
-  const Span read[] = {{k, kb}, {v, vb}, {q, qb}, {block_table, tb}, {rot_dim ? cos_sin : nullptr, cb},
-                       {new_lens, new_lens ? lb : 0}, {seq_lens, lb}};
-  for (const Span& w : written)
-    for (const Span& r : read) {
-      if (!overlap(w.p, w.n, r.p, r.n)) continue;
-      if ((w.p == q_out && r.p == q && q_in_place) || (w.p == seq_lens_out && r.p == seq_lens && w.p == r.p)) continue;
-      return WSVD_ERR_INVALID_ARG;
-    }
-  for (int i = 0; i < 4; ++i)
-    for (int j = i + 1; j < 4; ++j)
-      if (overlap(written[i].p, written[i].n, written[j].p, written[j].n)) return WSVD_ERR_INVALID_ARG;
+  const bool q_in_place = q_out == q && q_stride == (long long)Hq * Hd, lens_in_place = seq_lens_out == seq_lens;
+  const Span read[] = {span(k, k_stride, Hkv), span(v, v_stride, Hkv), span(q_in_place ? nullptr : q, q_stride, Hq),
+                       {block_table, (size_t)B * max_pages * 4}, {rot_dim ? cos_sin : nullptr, (size_t)max_pos * rot_dim * 4},
+                       {new_lens, lb}, {lens_in_place ? nullptr : seq_lens, lb}};
+  const Span written[] = {{k_pages, pool}, {v_pages, pool}, {q_out, tok * Hq * Hd * 2}, {seq_lens_out, lb},
+                          {workspace, paged_kv_append_workspace_size(B)}, {err, 4}};
+  if (wide || clash(written, read)) return WSVD_ERR_INVALID_ARG;
   if (workspace_bytes < paged_kv_append_workspace_size(B)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
 
   KvAppendArgs a{};
@@ -1130,7 +1129,14 @@ int paged_decode_attention(int B, int Tq, int Hq, int Hkv, int Hd, int page_size
   if (!seq_lens || !block_table || !q || !k_pages || !v_pages || !out || !workspace) return WSVD_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
     return WSVD_ERR_INVALID_ARG;
-  if (workspace_bytes < decode_ws(B, Tq, Hq, Hkv, Hd)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = decode_ws(B, Tq, Hq, Hkv, Hd), queries = (size_t)B * Tq * Hq * Hd;
+  size_t pool;
+  if (!pool_bytes(num_pages, Hkv, shift, (size_t)Hd * 2, &pool)) return WSVD_ERR_UNSUPPORTED;
+  const Span read[] = {{seq_lens, (size_t)B * 4}, {block_table, (size_t)B * max_pages * 4}, {q, queries * 2},
+                       {k_pages, pool}, {v_pages, pool}};
+  const Span written[] = {{out, queries * 4}, {workspace, need}, {err, 4}};
+  if (clash(written, read)) return WSVD_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return WSVD_ERR_WORKSPACE_TOO_SMALL;
   const int qc = chunk_queries((int)nq, Hd);
   const bool many = (long long)B * Hkv * ((nq + qc - 1) / qc) >= kSoloUnits;
   const DecodeKernel kern = dtype == WSVD_DTYPE_BF16 ? pick_decode<true>(Hd, qc, many) : pick_decode<false>(Hd, qc, many);

@@ -192,10 +192,31 @@ inline int page_shift_of(int page_size) {
   return -1;
 }
 
-// Whether [p, p + np) and [q, q + nq) share a byte.
-inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return np && nq && a < b + nq && b < a + np;
+// The bytes of an argument.
+struct Span {
+  const void* p;
+  size_t n;
+};
+inline bool overlap(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.p && y.p && x.n && y.n && a < b + y.n && b < a + x.n;
+}
+// Whether something that is written shares a byte with something that is read or
+// with another thing that is written.
+template <int W, int R>
+bool clash(const Span (&written)[W], const Span (&read)[R]) {
+  for (int i = 0; i < W; ++i) {
+    for (const Span& r : read)
+      if (overlap(written[i], r)) return true;
+    for (int j = i + 1; j < W; ++j)
+      if (overlap(written[i], written[j])) return true;
+  }
+  return false;
+}
+// *bytes = num_pages * heads * page_size rows of row_bytes; false past 2^63.
+inline bool pool_bytes(int num_pages, int heads, int page_shift, size_t row_bytes, size_t* bytes) {
+  return !__builtin_mul_overflow((size_t)num_pages * (size_t)heads, row_bytes << page_shift, bytes) &&
+         *bytes <= (size_t)1 << 63;
 }
 
 // CTAs of a kernel that the current device holds at once, at most

@@ -619,7 +619,15 @@ extern "C" int wsvd_decode_attention_paged(int B, int H, int Hd, int r, int bits
     return WSVD_ERR_INVALID_ARG;
   // The workspace of wsvd_decode_attention: the counters where that call has
   // them, so that calls of both, of any sizes, may use it in turn.
-  if (workspace_bytes < wsvd_decode_workspace_size(B, H, r)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = wsvd_decode_workspace_size(B, H, r), heads = (size_t)B * H, up = (size_t)H * r * Hd * 2;
+  size_t codes, scales;
+  if (!pool_bytes(num_pages, H, shift, (size_t)r * bits / 8, &codes) || !pool_bytes(num_pages, H, shift, 2, &scales))
+    return WSVD_ERR_UNSUPPORTED;
+  const Span read[] = {{seq_lens, (size_t)B * 4}, {block_table, (size_t)B * max_pages * 4}, {q, heads * Hd * 2},
+                       {lat_k, codes}, {lat_v, codes}, {scale_k, scales}, {scale_v, scales}, {B_k, up}, {B_v, up}};
+  const Span written[] = {{out, heads * Hd * 4}, {workspace, need}, {err, 4}};
+  if (clash(written, read)) return WSVD_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return WSVD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   LatDecodeArgs a{};
   a.seqs = PagedSeqs{B, H, max_pages << shift, seq_lens};
@@ -668,14 +676,21 @@ extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int b
   if (!aligned16(x) || !aligned16(A_k) || !aligned16(A_v) || !aligned16(lat_k) || !aligned16(lat_v) ||
       !aligned16(scale_k) || !aligned16(scale_v) || !aligned16(workspace))
     return WSVD_ERR_INVALID_ARG;
-  if (seq_lens_out != seq_lens && overlap(seq_lens_out, (size_t)B * 4, seq_lens, (size_t)B * 4))
-    return WSVD_ERR_INVALID_ARG;
-  if (overlap(seq_lens_out, (size_t)B * 4, block_table, (size_t)B * max_pages * 4)) return WSVD_ERR_INVALID_ARG;
   const int ranks = append_cluster_size(E, hadamard_block);
   const bool gemm = paged_block_takes(B, T, H, E, r);
   const bool gemv = T == 1 && B <= 16 && E <= 65536 && ranks > 0 && append_smem_bytes(B, E, r, ranks) <= 200 * 1024;
   if (T > 0 && !gemm && !gemv) return WSVD_ERR_UNSUPPORTED;
-  if (workspace_bytes < wsvd_latent_append_paged_workspace_size(B, T, E)) return WSVD_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = wsvd_latent_append_paged_workspace_size(B, T, E), lb = (size_t)B * 4;
+  const size_t xb = (size_t)B * T * E * 2, down = (size_t)H * E * r * 2;
+  size_t codes, scales;
+  if (!pool_bytes(num_pages, H, shift, (size_t)r * bits / 8, &codes) || !pool_bytes(num_pages, H, shift, 2, &scales))
+    return WSVD_ERR_UNSUPPORTED;
+  const Span read[] = {{seq_lens_out == seq_lens ? nullptr : seq_lens, lb}, {block_table, (size_t)B * max_pages * 4},
+                       {x, xb}, {A_k, down}, {A_v, down}};
+  const Span written[] = {{seq_lens_out, lb}, {lat_k, codes}, {lat_v, codes}, {scale_k, scales}, {scale_v, scales},
+                          {workspace, need}, {err, 4}};
+  if (clash(written, read)) return WSVD_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return WSVD_ERR_WORKSPACE_TOO_SMALL;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T == 0) {

@@ -239,8 +239,9 @@ def test_an_allowance_catches_planted_mistakes():
 
 def test_latent_append_refuses_blocks_of_too_many_tiles(lib):
     """B * T * H * r past 2^42, each within its own limit."""
-    assert lib.wsvd_latent_append_paged(*_lat_append_args(B=1 << 12, T=1 << 12, H=1 << 14, E=64, blk=64)) == 2
-    assert lib.wsvd_latent_append_paged(*_lat_append_args(B=1 << 12, T=1 << 12, H=1 << 13, E=64, blk=64)) == 4  # the workspace
+    apart = {k: _at((i + 1) << 20) for i, k in enumerate(("x", "Ak", "Av", "table", "lk", "lv", "sk", "sv", "ws"))}
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(B=1 << 12, T=1 << 12, H=1 << 14, E=64, blk=64, **apart)) == 2
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(B=1 << 12, T=1 << 12, H=1 << 13, E=64, blk=64, **apart)) == 4  # the workspace
 
 
 @pytest.mark.parametrize("TS", [16, 32, 64, 128])
@@ -254,3 +255,45 @@ def test_strips_of_lengths_at_the_end_of_the_range(TS):
         s = strips - 1
         assert (wrap(s * TS) > wrap(n - TS)) == (n % TS != 0)
         assert all(wrap(s * TS + i) == s * TS + i for i in (0, TS - 16, TS - 1))
+
+
+def _lat_pools(at):
+    """Every way two of the latent append's outputs, or one and an input, may meet."""
+    names = ("lk", "lv", "sk", "sv")
+    return [{a: at[b]} for a in names for b in names if a < b] + [{a: at[b]} for a in names for b in ("x", "Ak", "Av", "table", "ws")]
+
+
+AT = dict(x=_at(1), Ak=_at(2), Av=_at(3), table=_at(5), lk=_at(6), lv=_at(7), sk=_at(8), sv=_at(9), ws=_at(10))
+
+
+@pytest.mark.parametrize("kw", _lat_pools(AT) + [dict(lens=_at(6), out=_at(6)), dict(out=_at(9)), dict(ws=_at(2)),
+                                                 dict(lv=ctypes.c_void_p(6 * MIB + 16)), dict(err=_at(5)), dict(err=_at(8)),
+                                                 dict(lens=_at(10), out=_at(10))])
+def test_latent_append_refuses_overlaps(lib, kw):
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(**kw)) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(out=_at(i)) for i in (1, 2, 3, 4, 5, 7)] + [dict(ws=_at(i)) for i in range(1, 7)]
+                         + [dict(out=ctypes.c_void_p(4 * MIB - 16)), dict(err=_at(2)), dict(err=_at(7))])
+def test_kv_decode_refuses_overlaps(lib, kw):
+    assert lib.paged_decode_attention(*_decode_args(**kw)) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(out=_at(i)) for i in (1, 2, 3, 4, 5, 6, 7, 8, 9, 11)] + [dict(ws=_at(i)) for i in range(1, 11)]
+                         + [dict(err=_at(10)), dict(err=_at(8))])
+def test_latent_decode_refuses_overlaps(lib, kw):
+    assert lib.wsvd_decode_attention_paged(*_lat_decode_args(**kw)) == 1
+
+
+@pytest.mark.parametrize("kw,want", [(dict(ws=_at(i)), 1) for i in (1, 2, 3, 4, 5, 6, 7, 8)] + [
+    (dict(err=_at(7)), 1), (dict(err=_at(6)), 1), (dict(ks=1 << 62), 1), (dict(vs=1 << 61), 1), (dict(qs=(1 << 63) - 8), 1),
+    (dict(pages=2 ** 31 - 1, Hkv=1 << 18, Hq=0, q=None, qo=None, ks=1 << 26, vs=1 << 26, Hd=256, rot=0, cs=None, page=256), 2)])
+def test_kv_append_refuses_more_overlaps_and_impossible_strides(lib, kw, want):
+    assert lib.paged_kv_append(*_append_args(**kw)) == want
+
+
+def test_pools_past_every_address_are_refused(lib):
+    big = dict(pages=2 ** 31 - 1, page=256)
+    assert lib.paged_decode_attention(*_decode_args(Hq=1 << 20, Hkv=1 << 20, Hd=256, **big)) == 2
+    assert lib.wsvd_decode_attention_paged(*_lat_decode_args(H=1 << 20, r=128, **big)) == 2
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(H=1 << 20, r=128, **big)) == 2
