@@ -519,7 +519,9 @@ int paged_kv_append(int B, int T, int Hq, int Hkv, int Hd, int rot_dim, int inte
  * fp32 accumulation; the weights enter the product with V with 22 (fp16) or 24
  * (bf16) significant bits.  Rows >= seq_lens[b] are never read, and rows that a
  * query does not see never reach it, whatever they hold (infinities and NaN
- * included).  An infinite value in a row that is seen gives NaN.
+ * included).  In rows that are seen, a key whose logit is minus infinity weighs
+ * nothing, one of plus infinity or NaN makes the query's output NaN, and an
+ * infinite or NaN value leaves its column infinite or NaN.
  *   q         [B][Tq][Hq][Hd] of the pages' type (dtype).
  *   out       [B][Tq][Hq][Hd] float32, written.
  *   softmax_scale 0 selects 1/sqrt(Hd).

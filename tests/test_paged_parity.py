@@ -547,3 +547,45 @@ def test_paged_decode_matches_the_contiguous_one():
     ref, mass, wobble = P.decode(f64(q)[:, None], f64(kp.nan_to_num(0)), f64(vp.nan_to_num(0)), table, lens)
     allow = P.decode_allowance(mass, wobble, Hd, 520)[:, 0]
     assert err == 0 and (np.abs(f64(paged) - ref[:, 0]) <= allow).all() and (np.abs(f64(dense) - ref[:, 0]) <= allow).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("Hd", [32, 64, 128, 256])
+@pytest.mark.parametrize("G,Tq", [(2, 1), (16, 1), (3, 2)])
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_decode_infinite_keys_and_values_that_are_seen(dtype, Hd, G, Tq, scale):
+    """Infinite keys go by the formula: a logit of minus infinity weighs nothing, one
+    of plus infinity or NaN (and no finite logit at all) makes the output NaN.  An
+    infinite value leaves its column not finite, and the others as they were."""
+    lens = [40, 70, 33, 2]
+    kp, vp, table = _cache(lens, 1, Hd, 16, dtype, seed=51)
+    kp, vp = kp.nan_to_num(0), vp.nan_to_num(0)
+    q = randn((4, Tq, G, Hd), dtype, 52)
+    q[:, :, 0, 3] = 1.0
+    q[:, :, 1:, 3] = -1.0
+    inf = float("inf")
+    kp[table[0, 1], 0, 4, 3] = inf       # row 20 of sequence 0
+    kp[table[1, 2], 0, 5, 3] = -inf      # row 37 of sequence 1
+    kp[table[3, 0], 0, 0, 3] = inf       # row 0 of sequence 3: all that its token 0 of 2 sees
+    clean = vp.clone()
+    vp[table[2, 1], 0, 0, 7] = inf       # row 16 of sequence 2
+    out, err = _decode(q, kp, vp, table, lens, softmax_scale=scale)
+    assert err == 0
+    K, Q = f64(kp), f64(q)
+    s = scale or Hd ** -0.5
+    for b, n in enumerate(lens):
+        Kb, Vb = (P.rows(x, table, b, n)[:, 0] for x in (K, f64(clean)))
+        for t in range(Tq):
+            m = n - Tq + 1 + t
+            for g in range(G):
+                with np.errstate(invalid="ignore"):
+                    logit = (Kb[:m] * Q[b, t, g]).sum(1) * s
+                    p = np.exp(logit - logit.max())
+                    want = p @ Vb[:m] / p.sum()
+                got = f64(out[b, t, g])
+                if b == 2:
+                    assert not np.isfinite(got[7])
+                    want, got = np.delete(want, 7), np.delete(got, 7)
+                assert np.array_equal(np.isnan(got), np.isnan(want))
+                if not np.isnan(want).any():  # values below six, sums of |q_d k_d| scale below 64
+                    assert np.abs(got - want).max() <= P.decode_allowance(np.full(1, 6.0), np.full(1, 64.0), Hd, n).max()
