@@ -160,3 +160,34 @@ def test_one_token_by_the_append_kernel_has_its_bits(B, H, E, r, blk):
     for got, want in zip(lat + sc, flat + fsc):
         for b, l in enumerate(lens):
             assert torch.equal(got[table[b, l // page], :, l % page], want[b, :, l]) and want[b, :, l].any()
+
+
+@pytest.mark.gpu
+def test_a_prompt_repeats_its_bits_with_other_calls_between():
+    """576 tokens of 32 heads, E 4096, again and again with another prompt between and
+    nothing awaited: the same bytes each time, and those of a fresh cache."""
+    from rank_kv_cache_wsvd_b200 import build
+    build.build()
+    B, T, H, E, r, page = 1, 576, 32, 4096, 32, 64
+    table, pool = table_for([T], page, 1)
+    tab, n = cuda(table), torch.zeros(1, dtype=torch.int32, device="cuda")
+    to = torch.zeros_like(n)
+    x = [randn((B, T, E), "bf16", s) for s in (1, 2)]
+    down = [(randn((H, E, r), "fp16", s) * E ** -0.5).contiguous() for s in (4, 5)]
+    ws = W.workspace(W.wsvd_latent_append_paged_workspace_size(B, T, E))
+    empty = lambda: [torch.zeros((pool, H, page, r), dtype=torch.uint8, device="cuda") for _ in range(2)] + \
+        [torch.zeros((pool, H, page), dtype=torch.float16, device="cuda") for _ in range(2)]
+    cache, other = empty(), empty()
+    call = lambda i, c: W.wsvd_latent_append_paged(x[i], *down, n, tab, *c, 8, 128, seq_lens_out=to, workspace_buf=ws)
+    call(0, cache)
+    first = [t.clone() for t in cache]
+    for _ in range(20):
+        call(1, other)
+        call(0, cache)
+        call(1, cache)
+        call(0, cache)
+        for got, want in zip(cache, first):
+            assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    fresh = empty()
+    call(0, fresh)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(fresh, first))

@@ -418,3 +418,79 @@ def test_latent_append_of_no_tokens_copies_the_lengths():
     W.wsvd_latent_append_paged(torch.empty((2, 0, E), dtype=torch.bfloat16, device="cuda"), Ak, Av, n, cuda(table), lk, lv,
                                sk, sv, 8, 128, seq_lens_out=to)
     assert to.tolist() == [5, 9]
+
+
+def _strip_allowance(q, cache, Bk, Bv, lens, bits):
+    """How far the cut of the weights to 22 bits may take an output, [B][H][Hd]: a
+    weight w_l = p_l s_l is off by half a step of 2^-21 of the largest of its strip
+    (128, 64 or 32 rows, for rows of up to 32, 64 and 128 bytes), and meets its codes
+    and B_v: sum over strips of 2^-22 max w . sum |code| |B_v|."""
+    lk, lv, sk, sv, table = cache
+    TS = {16: 128, 32: 128, 64: 64, 128: 32}[lk.shape[-1]]
+    ck, cv = (P.latent_codes(t.cpu().numpy(), bits) for t in (lk, lv))
+    sk, sv = (np.nan_to_num(f64(t))[..., None] for t in (sk, sv))
+    out = np.zeros(q.shape)
+    for b, n in enumerate(lens):
+        K, C, S = P.rows(ck * sk, table, b, n), np.abs(P.rows(cv, table, b, n)), np.abs(P.rows(sv, table, b, n))
+        for h in range(q.shape[1]):
+            s = K[:, h] @ f64(Bk[h]) @ f64(q[b, h]) * q.shape[-1] ** -0.5
+            p = np.exp(s - s.max())
+            w = p / p.sum() * S[:, h, 0]
+            for at in range(0, n, TS):
+                out[b, h] += 2.0 ** -22 * w[at:at + TS].max() * C[at:at + TS, h].sum(0) @ np.abs(f64(Bv[h]))
+    return out
+
+
+def _uneven(bits, r, seed):
+    """Value scales over seven orders of magnitude, by row, by strip and by head."""
+    lens, H = [400, 261, 130], 4
+    cache = _cache(lens, H, r, bits, 16, seed=seed, poison=False)
+    table, sv = cache[4], cache[3]
+    sv[:, 0] *= 2.0 ** -9                            # a whole head of small rows beside large ones
+    sv[:, 1, ::2] *= 2.0 ** -8                       # every other row
+    for b, n in enumerate(lens):
+        for l in range(0, n, 2):
+            if (l // 32) % 2:                        # whole strips
+                sv[table[b, l // 16], 2, l % 16:l % 16 + 2] *= 2.0 ** -7
+    sv[:, 3, 5::16] *= 512                           # a few rows far above the others
+    return cache, lens, H
+
+
+@pytest.mark.parametrize("equal", [False, True])
+@pytest.mark.parametrize("bits,r", RANKS)
+def test_latent_decode_keeps_small_rows_beside_large_ones(bits, r, equal):
+    """A row is lost only where it lies 22 bits below the largest of its own strip;
+    with a query of zeros (all rows weigh the same) the allowance has no share of the
+    logits' rounding and lies below 1e-4 of what each output sums."""
+    (cache, lens, H), Hd = _uneven(bits, r, r), 64
+    lk, lv, sk, sv, table = cache
+    Bk, Bv = _factors(H, r, Hd, 8)
+    q = randn((3, H, Hd), "bf16", 9)
+    if equal:
+        q.zero_()
+    out, err = _decode(q, cache, Bk, Bv, lens, bits)
+    assert err == 0
+    ref, mass, wobble = P.latent_decode(f64(q), lk.cpu().numpy(), lv.cpu().numpy(), f64(sk), f64(sv), f64(Bk), f64(Bv),
+                                        table, lens, bits)
+    allow = P.latent_allowance(mass, wobble, r, Hd, np.zeros(1), max(lens)) + _strip_allowance(q, cache, Bk, Bv, lens, bits)
+    got = f64(out)
+    assert np.isfinite(got).all() and (np.abs(got - ref) <= allow).all()
+    # 2^-19 + (400 / 16 + 64 + 128) 2^-22 of the mass, and per strip at most 2^-22 x its rows x its largest share
+    assert not equal or (allow <= 1e-4 * mass).all()
+
+
+@pytest.mark.parametrize("bits,r", RANKS)
+def test_latent_decode_of_scaled_values_has_scaled_bits(bits, r):
+    """Value scales halved some times: every output halves as often, bit for bit, since
+    weights are cut relative to their strip."""
+    lens, H, Hd = [700, 33], 3, 64
+    lk, lv, sk, sv, table = _cache(lens, H, r, bits, 16, seed=r, poison=False)
+    Bk, Bv = _factors(H, r, Hd, 8)
+    q = randn((2, H, Hd), "bf16", 9)
+    sv = (sv.float() * 2.0 ** 8).half()
+    want, _ = _decode(q, (lk, lv, sk, sv, table), Bk, Bv, lens, bits)
+    by = torch.tensor([2.0 ** -3, 2.0 ** -9, 1.0], device="cuda")
+    small = sv * by.half().view(1, H, 1)
+    assert torch.equal(small.float() / by.view(1, H, 1), sv.float())  # no scale was rounded
+    out, _ = _decode(q, (lk, lv, sk, small, table), Bk, Bv, lens, bits)
+    assert torch.equal(out, want * by.view(1, H, 1))
