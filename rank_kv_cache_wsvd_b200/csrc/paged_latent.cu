@@ -678,7 +678,8 @@ extern "C" int wsvd_latent_append_paged(int B, int T, int H, int E, int r, int b
     return WSVD_ERR_INVALID_ARG;
   const int ranks = append_cluster_size(E, hadamard_block);
   const bool gemm = paged_block_takes(B, T, H, E, r);
-  const bool gemv = T == 1 && B <= 16 && E <= 65536 && ranks > 0 && append_smem_bytes(B, E, r, ranks) <= 200 * 1024;
+  const bool gemv = T == 1 && B <= 16 && E <= 65536 && 2LL * H <= 65535 && ranks > 0 &&
+                    append_smem_bytes(B, E, r, ranks) <= 200 * 1024;  // K and V of a head are grid rows
   if (T > 0 && !gemm && !gemv) return WSVD_ERR_UNSUPPORTED;
   const size_t need = wsvd_latent_append_paged_workspace_size(B, T, E), lb = (size_t)B * 4;
   const size_t xb = (size_t)B * T * E * 2, down = (size_t)H * E * r * 2;

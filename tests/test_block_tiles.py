@@ -191,3 +191,22 @@ def test_a_prompt_repeats_its_bits_with_other_calls_between():
     fresh = empty()
     call(0, fresh)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(fresh, first))
+
+
+@pytest.mark.gpu
+def test_one_token_of_more_heads_than_the_append_takes():
+    """33000 heads: the append's grid has no rows for them, the block kernel takes them."""
+    from rank_kv_cache_wsvd_b200 import build
+    build.build()
+    H, E, r, page = 33000, 64, 16, 16
+    x = randn((1, 1, E), "bf16", 3)
+    down = [randn((H, E, r), "fp16", s) * E ** -0.5 for s in (4, 5)]
+    lat = [torch.zeros((1, H, page, r), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    sc = [torch.zeros((1, H, page), dtype=torch.float16, device="cuda") for _ in range(2)]
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    W.wsvd_latent_append_paged(x, *down, n, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), *lat, *sc, 8, 64)
+    assert n.tolist() == [1]
+    for k in range(2):
+        c = torch.einsum("e,her->hr", _rotated(x, 64)[0, 0], down[k].double())
+        ties = _check_rows(lat[k][0, :, 0].view(torch.int8), sc[k][0, :, 0], c, 127)
+        assert ties <= 4 + H * (r * 2e-3 + 2.0 ** -8)

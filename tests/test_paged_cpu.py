@@ -292,6 +292,14 @@ def test_kv_append_refuses_more_overlaps_and_impossible_strides(lib, kw, want):
     assert lib.paged_kv_append(*_append_args(**kw)) == want
 
 
+def test_latent_append_of_more_heads_than_grid_rows_is_refused_where_only_the_append_takes_e(lib):
+    """E 272 is the append's alone, whose grid has a row for K and one for V of a head."""
+    args = dict(T=1, B=1, E=272, blk=16, r=16, x=_at(1 << 10), Ak=_at(1 << 12), Av=_at(1 << 13), lk=_at(1 << 14), lv=_at(1 << 15),
+                sk=_at(1 << 16), sv=_at(1 << 17), wsb=128)
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(H=32768, **args)) == 2
+    assert lib.wsvd_latent_append_paged(*_lat_append_args(H=32767, **args)) == 4  # the workspace
+
+
 def test_pools_past_every_address_are_refused(lib):
     big = dict(pages=2 ** 31 - 1, page=256)
     assert lib.paged_decode_attention(*_decode_args(Hq=1 << 20, Hkv=1 << 20, Hd=256, **big)) == 2
