@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kAppendCta) kv_append_kernel(const KvAppendArg
 template <bool BF16, int HD, int NB>
 struct DecCfg {
   // Rows per strip, warps per CTA and stages per warp: strips of 8 KB (16 KB at
-  // head size 256), 192 KB of them per SM.  Twelve warps of two stages beat
+  // head size 256), a ring of 192 KB per SM.  A warp reads one stage while the others
+  // are on their way: 96 KB an SM with two stages.  Twelve warps of two stages beat
   // eight of three (4 x 32768 rows of 8 heads of 128: 84.7 us against 87.3) except with
   // 16 queries of head size 128 and their registers (16 sequences of 1024 .. 4096 rows
   // of 8 heads 41.5 against 38.8, 4 x 32768 rows 92.7 against 94.5).  Strips of half the

@@ -22,10 +22,11 @@
 //              rounding to nearest (the tensor cores' own sums do not).
 // Where there are few tiles a cluster of up to 8 CTAs splits E for one tile; the
 // ranks' sums are read through the cluster's shared memory in rank order, each
-// rank quantising its share of the tokens.  Bound by the operand tiles' way from L2
-// (75 to 90 GB/s a SM whatever the tile): 32 heads of r 32, E 4096, both kernels:
-// 576 tokens 30.7 us (221 MB of tiles; the products alone, hi and lo, 11.7), 4096 tokens
-// 160 (1.0 GB; 83), 16 tokens 14.
+// rank quantising its share of the tokens.  The k-loop is bound by the operand tiles'
+// way from L2 (75 to 92 GB/s a SM whatever the tile).  32 heads of r 32, E 4096, both
+// kernels: 576 tokens 31 us, of which 16.7 are 32 k-tiles a CTA (221 MB of tiles; the
+// products alone, hi and lo, 11.7) and 14.4 do not grow with E (rotation, start, the
+// clusters' join, quantiser); 4096 tokens 160 (1.0 GB; 83), 16 tokens 14.5 (11.6 at E 1024).
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
