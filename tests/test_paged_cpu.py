@@ -305,3 +305,72 @@ def test_pools_past_every_address_are_refused(lib):
     assert lib.paged_decode_attention(*_decode_args(Hq=1 << 20, Hkv=1 << 20, Hd=256, **big)) == 2
     assert lib.wsvd_decode_attention_paged(*_lat_decode_args(H=1 << 20, r=128, **big)) == 2
     assert lib.wsvd_latent_append_paged(*_lat_append_args(H=1 << 20, r=128, **big)) == 2
+
+
+# ----------------------------------------------------------------------------- how strips are dealt
+def _deal(lens, units, TS, count, least, lead):
+    """The shares of the decodes' workers: [worker][(sequence * units + unit, first strip, end)], and the holders of a
+    unit's strips by the device's formula."""
+    sizes = [(b * units + u, -(-n // TS)) for b, n in enumerate(lens) if n > 0 for u in range(units)]
+    total = sum(n + lead for _, n in sizes)
+    workers = min(count, -(-total // least))
+    base, extra = divmod(total, workers)
+    begin = lambda c: base * c + min(c, extra)
+    worker_of = lambda s: s // (base + 1) if s < extra * (base + 1) else extra + (s - extra * (base + 1)) // base
+    shares, holders, at = [[] for _ in range(workers)], {}, 0
+    for key, n in sizes:
+        first, last = worker_of(at + lead), worker_of(at + lead + n - 1)
+        holders[key] = (first, last - first + 1)
+        c = worker_of(at)
+        while c < workers and begin(c) < at + lead + n:
+            s, e = max(begin(c), at + lead), min(begin(c + 1) if c + 1 < workers else total, at + lead + n)
+            if e > s:
+                shares[c].append((key, s - at - lead, e - at - lead, n))
+            c += 1
+        at += n + lead
+    return shares, holders
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_a_worker_is_the_first_of_at_most_one_cut_unit(seed):
+    """Counters by a unit's first worker, and the slots of the partial results, are each one's own."""
+    rng = np.random.default_rng(seed)
+    TS, lead, least = int(rng.choice([16, 32, 64, 128])), int(rng.choice([2, 4, 24])), int(rng.choice([1, 6, 12]))
+    count = int(rng.choice([148, 1776, 1920, 2016]))
+    B, units, top = int(rng.integers(1, 70)), int(rng.integers(1, 40)), int(rng.choice([3, 300, 5000, 40000]))
+    lens = [int(n) for n in rng.integers(0, top, B)]
+    lens[0] = max(1, lens[0])
+    shares, holders = _deal(lens, units, TS, count, least, lead)
+    held, counters, slots, two = {}, {}, set(), set()
+    for c, segs in enumerate(shares):
+        for key, s, e, n in segs:
+            held.setdefault(key, []).append((c, s, e))
+            if (s, e) == (0, n):
+                continue
+            counters.setdefault(holders[key][0], set()).add(key)
+            assert (c + key) not in slots and c + key < count + B * units  # the latent decode's slot
+            slots.add(c + key)
+            assert (c, s == 0) not in two                                  # the dense decode's: one that it begins, one within
+            two.add((c, s == 0))
+    assert all(len(keys) == 1 for keys in counters.values()) and max(counters, default=0) < 2048
+    for key, parts in held.items():
+        assert [p[0] for p in parts] == list(range(holders[key][0], sum(holders[key])))
+        assert parts[0][1] == 0 and all(a[2] == b[1] for a, b in zip(parts, parts[1:]))
+    assert sum(p[-1][2] for p in held.values()) == sum(-(-n // TS) for n in lens) * units
+
+
+def test_workspaces_hold_the_counters_and_the_slots_of_every_worker(lib):
+    """8 KB of counters and the partial results of all workers lie within the sizes, from the smallest row to the largest."""
+    for B, H in ((1, 1), (3, 7), (4096, 32)):
+        for r in (16, 32, 64, 128):
+            assert 8192 + (1920 + B * H) * (r + 2) * 4 <= W.wsvd_decode_workspace_size(B, H, r) - B * H * r * 4
+        for R in (32, 64, 128, 256):
+            assert 8192 + (1920 + B * H) * (R + 2) * 4 <= W.dense_decode_workspace_size(B, H, R) - B * H * R * 4
+        for R in (128, 1024):
+            assert 8192 + (1920 + B * H) * (R + 2) * 4 <= W.shared_decode_workspace_size(B, H, R) - B * H * R * 4
+    for Hd in (32, 64, 128, 256):
+        for nq in range(1, 65):
+            qc = 16 if nq > 8 and Hd != 256 else 8
+            m = min(nq, qc)
+            slot = (m * Hd + (2 * m + 3) // 4 * 4) * 4
+            assert 8192 + 2 * (2016 if qc == 8 else 588) * slot <= W.paged_decode_workspace_size(1, 1, nq, 1, Hd)
